@@ -38,6 +38,16 @@ EXPORTED = ("lq_version", "lq_status_string", "lq_state_layout", "lq_state_bytes
             "lq_checkpoint_restore", "lq_window_rewind", "lq_decode_tokens",
             "lq_decode_step_packed")
 
+LQ_DECAY_TOKEN, LQ_DECAY_HEAD = 0, 1
+LQ_ROPE_HALF, LQ_ROPE_INTERLEAVED = 0, 1
+LQ_ROPE_NONE, LQ_ROPE_LINEAR, LQ_ROPE_NTK, LQ_ROPE_PARTS = range(4)
+LQ_NORM_RMS, LQ_NORM_MEAN = 0, 1
+LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_SIGMOID = range(3)
+
+# Every symbol include/leapquant_layer.h declares.
+EXPORTED_LAYER = ("lq_linear_decode_step", "lq_linear_workspace_bytes", "lq_linear_prefill",
+                  "lq_rotary_table", "lq_rotary", "lq_group_norm", "lq_get_error_word")
+
 
 class lq_config(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
@@ -60,7 +70,32 @@ class lq_state(ctypes.Structure):
                 ("buf_n", ctypes.c_void_p), ("err", ctypes.c_void_p)]
 
 
+class lq_linear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_k_heads", "num_v_heads", "dk", "dv", "decay", "in_dtype", "out_dtype")] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class lq_rotary_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_q_heads", "num_k_heads", "d", "rot", "layout", "dtype", "inverse")] + \
+        [("magnitude", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+class lq_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "groups", "size", "kind", "act", "gate_before", "shared_weight", "in_dtype",
+        "out_dtype")] + [("eps", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "out_stride")]
+
+
 _P = ctypes.c_void_p
+_I = ctypes.c_int32
+_F64 = ctypes.c_double
+_LIN = ctypes.POINTER(lq_linear_config)
+_ROT = ctypes.POINTER(lq_rotary_config)
+_NORM = ctypes.POINTER(lq_norm_config)
 _CFG = ctypes.POINTER(lq_config)
 _ST = ctypes.POINTER(lq_state)
 _sig = {
@@ -87,6 +122,15 @@ _sig = {
     "lq_window_rewind": ([_CFG, _ST, _P, _P], ctypes.c_int),
     "lq_decode_tokens": ([_CFG, ctypes.c_int32, _P, _P, _P, _P, _P, _ST, _P, _P, _P],
                          ctypes.c_int),
+    "lq_linear_decode_step": ([_LIN, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P], ctypes.c_int),
+    "lq_linear_workspace_bytes": ([_LIN, _I], ctypes.c_size_t),
+    "lq_linear_prefill": ([_LIN, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, ctypes.c_size_t,
+                           _P, _P], ctypes.c_int),
+    "lq_rotary_table": ([_I, _F64, _I, _F64, _F64, _F64, _F64, _P,
+                         ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
+    "lq_rotary": ([_ROT, _I, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "lq_group_norm": ([_NORM, _I, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "lq_get_error_word": ([_P, _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _f = getattr(_lib, _name)
@@ -299,6 +343,145 @@ def lq_state_dequantize(cfg, state: lq_state, include_buffer: bool, S_out, strea
 def lq_get_last_error(state: lq_state, stream=None) -> int:
     """Status word of the device-side checks (LQ_OK or LQ_ERR_DEVICE_BOUNDS)."""
     return _lib.lq_get_last_error(ctypes.byref(state), _stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# The layer operators (include/leapquant_layer.h), same names
+# ---------------------------------------------------------------------------
+
+def _here(x, what: str) -> Optional[int]:
+    """Address of a contiguous tensor on the current device (or an int, None)."""
+    if x is None or isinstance(x, int):
+        return x
+    _on_device(x, what)
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: the tensor must be contiguous")
+    return x.data_ptr()
+
+
+def _on_device(x, what: str) -> None:
+    import torch
+
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: the tensor must be on the current CUDA device")
+
+
+def _rows(x, stride: int, what: str) -> Optional[int]:
+    """Address of a token-major tensor [tokens, heads, d] on the current device
+    whose tokens lie `stride` elements apart (0: packed), each token's row
+    contiguous: a packed tensor or a slice of a fused projection's rows."""
+    if x is None or isinstance(x, int):
+        return x
+    _on_device(x, what)
+    if not x.is_contiguous() or stride:
+        n, s, row = x.shape, x.stride(), 1
+        for i in range(x.dim() - 1, 0, -1):
+            if n[i] != 1 and s[i] != row:
+                raise ValueError(f"{what}: a token's row must be contiguous")
+            row *= n[i]
+        if n[0] > 1 and row > 0 and s[0] != (stride or row):
+            raise ValueError(f"{what}: tokens lie {s[0]} elements apart, "
+                             f"the configuration says {stride or row}")
+    return x.data_ptr()
+
+
+def make_linear_config(batch: int, num_k_heads: int, num_v_heads: int, dk: int, dv: int,
+                       decay: int = LQ_DECAY_TOKEN, in_bf16: bool = False,
+                       out_bf16: bool = False, q_stride: int = 0, k_stride: int = 0,
+                       v_stride: int = 0) -> lq_linear_config:
+    return lq_linear_config(batch, num_k_heads, num_v_heads, dk, dv, decay,
+                            LQ_DTYPE_BF16 if in_bf16 else LQ_DTYPE_F32,
+                            LQ_DTYPE_BF16 if out_bf16 else LQ_DTYPE_F32, q_stride, k_stride,
+                            v_stride)
+
+
+def lq_linear_decode_step(cfg, q, k, v, decay, S, num_slots: int, out, err, slots=None,
+                          stream=None) -> None:
+    """One token of S <- a S + v k^T, o = S q for every sequence, states in
+    the pool S [num_slots, Hv, dv, dk] updated in place."""
+    _check(_lib.lq_linear_decode_step(
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
+        _rows(v, cfg.v_stride, "v"), _here(decay, "decay"), _here(S, "S"), num_slots,
+        _here(slots, "slots"), _here(out, "out"), _here(err, "err"), _stream(stream)),
+        "lq_linear_decode_step")
+
+
+def lq_linear_workspace_bytes(cfg, tokens: int) -> int:
+    return _lib.lq_linear_workspace_bytes(ctypes.byref(cfg), tokens)
+
+
+def lq_linear_prefill(cfg, q, k, v, decay, tokens: int, offsets, S, num_slots: int, out, err,
+                      slots=None, fresh=None, workspace=None, stream=None) -> None:
+    """The recurrence over packed prompts: sequence b owns rows
+    offsets[b] .. offsets[b + 1] - 1 of `tokens`.  out may be None."""
+    space = 0 if workspace is None or isinstance(workspace, int) else \
+        workspace.numel() * workspace.element_size()
+    if isinstance(workspace, int):
+        space = lq_linear_workspace_bytes(cfg, tokens)
+    _check(_lib.lq_linear_prefill(
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
+        _rows(v, cfg.v_stride, "v"), _here(decay, "decay"), tokens, _here(offsets, "offsets"),
+        _here(S, "S"), num_slots, _here(slots, "slots"), _here(fresh, "fresh"),
+        _here(out, "out"), _here(workspace, "workspace"), space, _here(err, "err"),
+        _stream(stream)), "lq_linear_prefill")
+
+
+def lq_rotary_table(rot: int, theta: float = 10000.0, scaling: int = LQ_ROPE_NONE,
+                    factor: float = 1.0, trained: float = 0.0, fast_turns: float = 32.0,
+                    slow_turns: float = 1.0):
+    """(table, magnitude): the rotation's table as an int64 host tensor
+    [rot / 2] (the entries' 64 bits), to be moved to the device once."""
+    import torch
+
+    table = torch.empty(max(rot // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_float(1.0)
+    _check(_lib.lq_rotary_table(rot, theta, scaling, factor, trained, fast_turns, slow_turns,
+                                table.data_ptr(), ctypes.byref(magnitude)), "lq_rotary_table")
+    return table, magnitude.value
+
+
+def make_rotary_config(num_q_heads: int, num_k_heads: int, d: int, rot: int,
+                       layout: int = LQ_ROPE_HALF, bf16: bool = True, magnitude: float = 1.0,
+                       inverse: bool = False, q_stride: int = 0, k_stride: int = 0,
+                       q_out_stride: int = 0, k_out_stride: int = 0) -> lq_rotary_config:
+    return lq_rotary_config(num_q_heads, num_k_heads, d, rot, layout,
+                            LQ_DTYPE_BF16 if bf16 else LQ_DTYPE_F32, 1 if inverse else 0,
+                            magnitude, q_stride, k_stride, q_out_stride, k_out_stride)
+
+
+def lq_rotary(cfg, tokens: int, q, k, positions, table, q_out, k_out, stream=None) -> None:
+    """Rotates q and k (None without k heads) into q_out and k_out, which may
+    be q and k themselves."""
+    _check(_lib.lq_rotary(
+        ctypes.byref(cfg), tokens, _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
+        _here(positions, "positions"), _here(table, "table"),
+        _rows(q_out, cfg.q_out_stride, "q_out"), _rows(k_out, cfg.k_out_stride, "k_out"),
+        _stream(stream)), "lq_rotary")
+
+
+def make_norm_config(groups: int, size: int, kind: int = LQ_NORM_RMS, act: int = LQ_ACT_SILU,
+                     gate_before: bool = False, shared_weight: bool = False,
+                     in_bf16: bool = False, out_bf16: bool = False, eps: float = 1e-5,
+                     x_stride: int = 0, gate_stride: int = 0,
+                     out_stride: int = 0) -> lq_norm_config:
+    return lq_norm_config(groups, size, kind, act, 1 if gate_before else 0,
+                          1 if shared_weight else 0, LQ_DTYPE_BF16 if in_bf16 else LQ_DTYPE_F32,
+                          LQ_DTYPE_BF16 if out_bf16 else LQ_DTYPE_F32, eps, x_stride,
+                          gate_stride, out_stride)
+
+
+def lq_group_norm(cfg, tokens: int, x, out, gate=None, weight=None, bias=None,
+                  stream=None) -> None:
+    """Normalises each token's groups; act on the result, or on the gate."""
+    _check(_lib.lq_group_norm(
+        ctypes.byref(cfg), tokens, _rows(x, cfg.x_stride, "x"),
+        _rows(gate, cfg.gate_stride, "gate"), _here(weight, "weight"), _here(bias, "bias"),
+        _rows(out, cfg.out_stride, "out"), _stream(stream)), "lq_group_norm")
+
+
+def lq_get_error_word(err, stream=None) -> int:
+    """Synchronizes the stream, reads and clears the error word."""
+    return _lib.lq_get_error_word(_here(err, "err"), _stream(stream))
 
 
 # ---------------------------------------------------------------------------

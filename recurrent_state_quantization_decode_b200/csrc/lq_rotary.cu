@@ -1,0 +1,143 @@
+// Rotary positions on q and k.
+//
+// The angle of pair i at position p is p f_i.  With f_i held as a 64-bit
+// fraction of a turn, the product modulo 2^64 is the angle modulo one turn,
+// exact for every int32 position: no argument reduction and no 64-bit
+// floating point, and the top 32 bits, read as signed, are the angle in
+// [-1/2, 1/2) turns to 2^-32.
+//
+// Bound by the bytes of q and k.  A block computes the sines and cosines of
+// its few tokens once (rot / 2 each) and applies them to all heads.
+
+#include "lq_chunk.cuh"
+#include "lq_layer.h"
+
+namespace lq {
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kMaxTok = 8;  // tokens of a block
+
+// A head is split into `turned` work items (a pair of chunks in the half
+// layout, one chunk of pairs interleaved) and the chunks behind rot.
+template <bool BF16, bool INTER, int VEC>
+__global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int tok, bool copy_q,
+                                                     bool copy_k) {
+  // the interleaved scalar form takes a pair at a time
+  constexpr int W = INTER && VEC == 1 ? 2 : VEC;
+  extern __shared__ float2 cs[];  // [tok][rot / 2] (cos, sin)
+  const int half = p.rot / 2, heads = p.Hq + p.Hk;
+  const int t0 = blockIdx.x * tok, nt = min(tok, p.tokens - t0);
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  for (int i = tid; i < nt * half; i += blockDim.x * blockDim.y) {
+    const int t = i / half;
+    const uint64_t turn = p.table[i - t * half] *
+                          static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + t]));
+    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;  // half turns
+    float s, c;
+    sincospif(x, &s, &c);
+    cs[i] = make_float2(c * p.cos_mul, s * p.sin_mul);
+  }
+  __syncthreads();
+  const int turned = INTER ? p.rot / W : half / VEC;
+  const int items = turned + (p.d - p.rot) / VEC;
+  // rows (token, head) over threadIdx.y and the grid's second axis
+  for (int r = blockIdx.y * blockDim.y + threadIdx.y; r < nt * heads; r += gridDim.y * blockDim.y) {
+    const int t = r / heads, hh = r - t * heads;
+    const bool is_q = hh < p.Hq;
+    const int head = is_q ? hh : hh - p.Hq;
+    const void *src = is_q ? p.q : p.k;
+    void *dst = is_q ? p.q_out : p.k_out;
+    const int64_t from = (t0 + t) * (is_q ? p.q_stride : p.k_stride) + head * p.d;
+    const int64_t to = (t0 + t) * (is_q ? p.q_out_stride : p.k_out_stride) + head * p.d;
+    const float2 *row = cs + t * half;
+    for (int c = threadIdx.x; c < items; c += blockDim.x) {
+      if (c >= turned) {
+        if (is_q ? copy_q : copy_k) {
+          Chunk<BF16, VEC> x;
+          const int at = p.rot + (c - turned) * VEC;
+          x.load(src, from + at);
+          x.store(dst, to + at);
+        }
+      } else if constexpr (!INTER) {
+        Chunk<BF16, VEC> a, b;
+        const int at = c * VEC;
+        a.load(src, from + at);
+        b.load(src, from + half + at);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float2 w = row[at + j];
+          const float x = a.x[j], y = b.x[j];
+          a.x[j] = x * w.x - y * w.y;
+          b.x[j] = y * w.x + x * w.y;
+        }
+        a.store(dst, to + at);
+        b.store(dst, to + half + at);
+      } else if constexpr (VEC == 1) {
+        Chunk<BF16, 1> a, b;
+        a.load(src, from + 2 * c);
+        b.load(src, from + 2 * c + 1);
+        const float2 w = row[c];
+        const float x = a.x[0], y = b.x[0];
+        a.x[0] = x * w.x - y * w.y;
+        b.x[0] = y * w.x + x * w.y;
+        a.store(dst, to + 2 * c);
+        b.store(dst, to + 2 * c + 1);
+      } else {
+        Chunk<BF16, VEC> a;
+        const int at = c * VEC;
+        a.load(src, from + at);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          const float2 w = row[at / 2 + j];
+          const float x = a.x[2 * j], y = a.x[2 * j + 1];
+          a.x[2 * j] = x * w.x - y * w.y;
+          a.x[2 * j + 1] = y * w.x + x * w.y;
+        }
+        a.store(dst, to + at);
+      }
+    }
+  }
+}
+
+template <bool BF16, bool INTER, int VEC>
+cudaError_t rotary_t(const RotaryParams &p, cudaStream_t st) {
+  const int half = p.rot / 2, heads = p.Hq + p.Hk;
+  const int items = (INTER ? (VEC == 1 ? half : p.rot / VEC) : half / VEC) + (p.d - p.rot) / VEC;
+  int bx = 1;
+  while (bx < items && bx < 128) bx *= 2;
+  const dim3 block(bx, kNT / bx);
+  // Several tokens share a block where that fills its threads with sines, but
+  // only as long as the blocks still fill the GPU twice over; few tokens
+  // instead split their heads over more blocks.
+  int tok = 1;
+  while (tok < kMaxTok && 2 * tok * half <= kNT && p.tokens / (2 * tok) >= 592) tok *= 2;
+  const int gx = (p.tokens + tok - 1) / tok;
+  const int rows = (tok * heads + block.y - 1) / block.y;
+  int gy = 1;
+  while (gy < rows && gx * gy < 296) gy *= 2;
+  rotary_kernel<BF16, INTER, VEC><<<dim3(gx, gy), block, tok * half * sizeof(float2), st>>>(
+      p, tok, p.q != p.q_out, p.k != p.k_out);
+  return cudaGetLastError();
+}
+
+template <bool BF16, bool INTER>
+cudaError_t rotary_v(const RotaryParams &p, cudaStream_t st) {
+  constexpr int VEC = BF16 ? 8 : 4;
+  bool wide = (INTER ? p.rot : p.rot / 2) % VEC == 0 && p.d % VEC == 0;
+  const void *ptr[4] = {p.q, p.q_out, p.k, p.k_out};
+  const int64_t stride[4] = {p.q_stride, p.q_out_stride, p.k_stride, p.k_out_stride};
+  for (int i = 0; i < 4; ++i)
+    if (i < 2 ? p.Hq > 0 : p.Hk > 0)
+      wide = wide && reinterpret_cast<uintptr_t>(ptr[i]) % 16 == 0 && stride[i] % VEC == 0;
+  return wide ? rotary_t<BF16, INTER, VEC>(p, st) : rotary_t<BF16, INTER, 1>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t st) {
+  if (p.bf16) return p.interleaved ? rotary_v<true, true>(p, st) : rotary_v<true, false>(p, st);
+  return p.interleaved ? rotary_v<false, true>(p, st) : rotary_v<false, false>(p, st);
+}
+
+}  // namespace lq
