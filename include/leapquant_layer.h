@@ -91,10 +91,12 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  *  workspace: lq_linear_workspace_bytes(cfg, tokens) bytes, 16-byte aligned
  *  (nullable when that is 0).  Its contents matter during the call only; calls
  *  that may run at the same time, captured ones too, need one each.
- *  - Prompts are taken in chunks whose products run on the tensor cores with
- *    fp32 accumulation and the state in fp32; decays enter as differences of
- *    summed logarithms, so that a decay of 0 (a reset) and long chains of
- *    small ones stay exact zeros instead of overflowing. */
+ *  - bf16 prompts are taken in chunks of 128 tokens whose products run on the
+ *    tensor cores with fp32 accumulation; states and fp32 outputs are fp32
+ *    results (operands go in as exact sums of bf16 parts), bf16 outputs may
+ *    see the state rounded once to bf16.  Decays enter as products over ranges
+ *    of tokens, never as quotients: a decay of 0 (a reset) and long chains of
+ *    small ones give exact zeros. */
 size_t lq_linear_workspace_bytes(const lq_linear_config *cfg, int32_t tokens);
 lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const void *k,
                             const void *v, const float *decay, int32_t tokens,

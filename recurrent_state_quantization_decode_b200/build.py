@@ -19,11 +19,11 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libleapquant.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("lq_decode.cu", "lq_fp32.cu", "lq_checkpoint.cu",
                                             "lq_hostio.cu", "lq_capi.cu", "lq_noalloc.cu",
-                                            "lq_linear.cu", "lq_rotary.cu", "lq_norm.cu",
-                                            "lq_layer_capi.cu")]
+                                            "lq_linear.cu", "lq_linear_mma.cu",
+                                            "lq_rotary.cu", "lq_norm.cu", "lq_layer_capi.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("lq_internal.h", "lq_checkpoint.h",
                                                           "lq_hostio.h", "lq_capi_internal.h", "lq_layer.h",
-                                                          "lq_linear_common.cuh",
+                                                          "lq_linear_common.cuh", "lq_tensor.cuh",
                                                           "lq_chunk.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("leapquant.h", "leapquant_layer.h")]
 

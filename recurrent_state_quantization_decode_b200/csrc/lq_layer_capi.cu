@@ -79,6 +79,9 @@ lq_status check_linear_io(const lq_linear_config *c, lq::LinParams *p, bool inpu
   return LQ_OK;
 }
 
+// Which prompt kernel a call takes: bf16 inputs go to the tensor cores.
+bool by_chunks(const lq::LinParams &p) { return p.in_bf16 != 0; }
+
 }  // namespace
 
 extern "C" {
@@ -100,7 +103,8 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
 size_t lq_linear_workspace_bytes(const lq_linear_config *cfg, int32_t tokens) {
   lq::LinParams p;
   if (check_linear(cfg, &p) != LQ_OK || tokens < 0) return 0;
-  return 0;
+  p.tokens = tokens;
+  return by_chunks(p) ? lq::linear_chunks_workspace(p) : 0;
 }
 
 lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const void *k,
@@ -123,7 +127,9 @@ lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const vo
   p.tokens = tokens;
   p.offsets = offsets;
   p.fresh = fresh;
-  return from_cuda(lq::launch_linear_prefill(p, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return from_cuda(by_chunks(p) ? lq::launch_linear_chunks(p, workspace, cs)
+                                : lq::launch_linear_tokens(p, cs));
 }
 
 lq_status lq_rotary_table(int32_t rot, double theta, int32_t scaling, double factor,

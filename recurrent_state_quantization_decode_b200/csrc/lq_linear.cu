@@ -171,7 +171,7 @@ cudaError_t launch_linear_step(const LinParams &p, cudaStream_t st) {
   return step_d<128>(p, st);
 }
 
-cudaError_t launch_linear_prefill(const LinParams &p, cudaStream_t st) {
+cudaError_t launch_linear_tokens(const LinParams &p, cudaStream_t st) {
   if (p.dk == 32) return tokens_d<32>(p, st);
   if (p.dk == 64) return tokens_d<64>(p, st);
   return tokens_d<128>(p, st);
