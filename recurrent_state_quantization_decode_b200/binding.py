@@ -349,31 +349,45 @@ def lq_get_last_error(state: lq_state, stream=None) -> int:
 # The layer operators (include/leapquant_layer.h), same names
 # ---------------------------------------------------------------------------
 
-def _here(x, what: str) -> Optional[int]:
+_torch = None
+
+
+def _current():
+    """(current device, current stream's handle) as torch has them; (-2, None)
+    before torch has a CUDA context."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized():
+        return -2, None
+    dev = _torch._C._cuda_getDevice()
+    return dev, _torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _here(x, dev: int, what: str) -> Optional[int]:
     """Address of a contiguous tensor on the current device (or an int, None)."""
     if x is None or isinstance(x, int):
         return x
-    _on_device(x, what)
+    if x.get_device() != dev:
+        raise ValueError(f"{what}: the tensor must be on the current CUDA device")
     if not x.is_contiguous():
         raise ValueError(f"{what}: the tensor must be contiguous")
     return x.data_ptr()
 
 
-def _on_device(x, what: str) -> None:
-    import torch
-
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: the tensor must be on the current CUDA device")
-
-
-def _rows(x, stride: int, what: str) -> Optional[int]:
+def _rows(x, stride: int, dev: int, what: str) -> Optional[int]:
     """Address of a token-major tensor [tokens, heads, d] on the current device
     whose tokens lie `stride` elements apart (0: packed), each token's row
     contiguous: a packed tensor or a slice of a fused projection's rows."""
     if x is None or isinstance(x, int):
         return x
-    _on_device(x, what)
-    if not x.is_contiguous() or stride:
+    if x.get_device() != dev:
+        raise ValueError(f"{what}: the tensor must be on the current CUDA device")
+    if stride and x.dim() == 3 and x.stride(2) == 1 and x.stride(1) == x.size(2) and \
+            x.stride(0) == stride:
+        return x.data_ptr()
+    if stride or not x.is_contiguous():
         n, s, row = x.shape, x.stride(), 1
         for i in range(x.dim() - 1, 0, -1):
             if n[i] != 1 and s[i] != row:
@@ -383,6 +397,13 @@ def _rows(x, stride: int, what: str) -> Optional[int]:
             raise ValueError(f"{what}: tokens lie {s[0]} elements apart, "
                              f"the configuration says {stride or row}")
     return x.data_ptr()
+
+
+def _on(stream, current) -> Optional[int]:
+    """The handle of a call's stream: the current one by default."""
+    if stream is None:
+        return current
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def make_linear_config(batch: int, num_k_heads: int, num_v_heads: int, dk: int, dv: int,
@@ -399,11 +420,12 @@ def lq_linear_decode_step(cfg, q, k, v, decay, S, num_slots: int, out, err, slot
                           stream=None) -> None:
     """One token of S <- a S + v k^T, o = S q for every sequence, states in
     the pool S [num_slots, Hv, dv, dk] updated in place."""
+    dev, now = _current()
     _check(_lib.lq_linear_decode_step(
-        ctypes.byref(cfg), _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
-        _rows(v, cfg.v_stride, "v"), _here(decay, "decay"), _here(S, "S"), num_slots,
-        _here(slots, "slots"), _here(out, "out"), _here(err, "err"), _stream(stream)),
-        "lq_linear_decode_step")
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q"), _rows(k, cfg.k_stride, dev, "k"),
+        _rows(v, cfg.v_stride, dev, "v"), _here(decay, dev, "decay"), _here(S, dev, "S"),
+        num_slots, _here(slots, dev, "slots"), _here(out, dev, "out"), _here(err, dev, "err"),
+        _on(stream, now)), "lq_linear_decode_step")
 
 
 def lq_linear_workspace_bytes(cfg, tokens: int) -> int:
@@ -414,16 +436,20 @@ def lq_linear_prefill(cfg, q, k, v, decay, tokens: int, offsets, S, num_slots: i
                       slots=None, fresh=None, workspace=None, stream=None) -> None:
     """The recurrence over packed prompts: sequence b owns rows
     offsets[b] .. offsets[b + 1] - 1 of `tokens`.  out may be None."""
-    space = 0 if workspace is None or isinstance(workspace, int) else \
-        workspace.numel() * workspace.element_size()
-    if isinstance(workspace, int):
+    dev, now = _current()
+    if workspace is None:
+        space = 0
+    elif isinstance(workspace, int):
         space = lq_linear_workspace_bytes(cfg, tokens)
+    else:
+        space = workspace.nbytes
     _check(_lib.lq_linear_prefill(
-        ctypes.byref(cfg), _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
-        _rows(v, cfg.v_stride, "v"), _here(decay, "decay"), tokens, _here(offsets, "offsets"),
-        _here(S, "S"), num_slots, _here(slots, "slots"), _here(fresh, "fresh"),
-        _here(out, "out"), _here(workspace, "workspace"), space, _here(err, "err"),
-        _stream(stream)), "lq_linear_prefill")
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q"), _rows(k, cfg.k_stride, dev, "k"),
+        _rows(v, cfg.v_stride, dev, "v"), _here(decay, dev, "decay"), tokens,
+        _here(offsets, dev, "offsets"), _here(S, dev, "S"), num_slots,
+        _here(slots, dev, "slots"), _here(fresh, dev, "fresh"), _here(out, dev, "out"),
+        _here(workspace, dev, "workspace"), space, _here(err, dev, "err"), _on(stream, now)),
+        "lq_linear_prefill")
 
 
 def lq_rotary_table(rot: int, theta: float = 10000.0, scaling: int = LQ_ROPE_NONE,
@@ -452,11 +478,12 @@ def make_rotary_config(num_q_heads: int, num_k_heads: int, d: int, rot: int,
 def lq_rotary(cfg, tokens: int, q, k, positions, table, q_out, k_out, stream=None) -> None:
     """Rotates q and k (None without k heads) into q_out and k_out, which may
     be q and k themselves."""
+    dev, now = _current()
     _check(_lib.lq_rotary(
-        ctypes.byref(cfg), tokens, _rows(q, cfg.q_stride, "q"), _rows(k, cfg.k_stride, "k"),
-        _here(positions, "positions"), _here(table, "table"),
-        _rows(q_out, cfg.q_out_stride, "q_out"), _rows(k_out, cfg.k_out_stride, "k_out"),
-        _stream(stream)), "lq_rotary")
+        ctypes.byref(cfg), tokens, _rows(q, cfg.q_stride, dev, "q"),
+        _rows(k, cfg.k_stride, dev, "k"), _here(positions, dev, "positions"),
+        _here(table, dev, "table"), _rows(q_out, cfg.q_out_stride, dev, "q_out"),
+        _rows(k_out, cfg.k_out_stride, dev, "k_out"), _on(stream, now)), "lq_rotary")
 
 
 def make_norm_config(groups: int, size: int, kind: int = LQ_NORM_RMS, act: int = LQ_ACT_SILU,
@@ -473,15 +500,18 @@ def make_norm_config(groups: int, size: int, kind: int = LQ_NORM_RMS, act: int =
 def lq_group_norm(cfg, tokens: int, x, out, gate=None, weight=None, bias=None,
                   stream=None) -> None:
     """Normalises each token's groups; act on the result, or on the gate."""
+    dev, now = _current()
     _check(_lib.lq_group_norm(
-        ctypes.byref(cfg), tokens, _rows(x, cfg.x_stride, "x"),
-        _rows(gate, cfg.gate_stride, "gate"), _here(weight, "weight"), _here(bias, "bias"),
-        _rows(out, cfg.out_stride, "out"), _stream(stream)), "lq_group_norm")
+        ctypes.byref(cfg), tokens, _rows(x, cfg.x_stride, dev, "x"),
+        _rows(gate, cfg.gate_stride, dev, "gate"), _here(weight, dev, "weight"),
+        _here(bias, dev, "bias"), _rows(out, cfg.out_stride, dev, "out"), _on(stream, now)),
+        "lq_group_norm")
 
 
 def lq_get_error_word(err, stream=None) -> int:
     """Synchronizes the stream, reads and clears the error word."""
-    return _lib.lq_get_error_word(_here(err, "err"), _stream(stream))
+    dev, now = _current()
+    return _lib.lq_get_error_word(_here(err, dev, "err"), _on(stream, now))
 
 
 # ---------------------------------------------------------------------------

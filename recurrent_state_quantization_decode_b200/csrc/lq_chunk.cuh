@@ -8,27 +8,43 @@
 
 namespace lq {
 
-// VEC consecutive values as fp32: 16 bytes at a time, or one value.
+// VEC consecutive values as they lie in memory: 16 bytes, or one value.
+template <bool BF16, int VEC>
+struct Raw {
+  uint4 v;
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * (BF16 ? 2 : 4));
+  }
+};
+template <bool BF16>
+struct Raw<BF16, 1> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    if constexpr (BF16)
+      v = static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16;
+    else
+      v = static_cast<const uint32_t *>(p)[i];
+  }
+};
+
+// The same as fp32.
 template <bool BF16, int VEC>
 struct Chunk {
   float x[VEC];
-  __device__ __forceinline__ void load(const void *p, int64_t i) {
+  __device__ __forceinline__ void set(const Raw<BF16, VEC> &r) {
     if constexpr (VEC == 1) {
-      if constexpr (BF16)
-        x[0] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-      else
-        x[0] = reinterpret_cast<const float *>(p)[i];
-    } else if constexpr (BF16) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      x[0] = __uint_as_float(r.v);
+    } else {
+      const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        if constexpr (BF16) {
+          x[2 * j] = __uint_as_float(w[j] << 16);
+          x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+          x[j] = __uint_as_float(w[j]);
+        }
       }
-    } else {
-      const float4 u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
     }
   }
   __device__ __forceinline__ void store(void *p, int64_t i) const { store_as<BF16>(p, i); }

@@ -39,6 +39,7 @@
 // their rounding would show), and S, whose roundings average over the key
 // channels, as one, to 2^-8 like the outputs themselves.
 
+#include <atomic>
 #include <cstddef>
 #include <type_traits>
 
@@ -1021,17 +1022,31 @@ template <int DKP, int DVP, bool F32OUT, bool STATES>
 cudaError_t launch_t(const LinParams &p, const Segments &sg, const CUtensorMap (&m)[4], int64_t grid,
                      cudaStream_t st) {
   auto kernel = linear_chunks_kernel<DKP, DVP, F32OUT, STATES>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Tiles<DKP, DVP>::kBytes);
+  // once for each device
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((ready.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Tiles<DKP, DVP>::kBytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   kernel<<<static_cast<unsigned>(grid), kNT, Tiles<DKP, DVP>::kBytes, st>>>(p, sg, m[0], m[1], m[2],
                                                                               m[3]);
   return cudaGetLastError();
 }
 
+// At most how many segments come before a sequence's last one.
+int64_t split_segments(const LinParams &p, int segment) {
+  return p.tokens > segment ? p.tokens / segment : 0;
+}
+
 template <int DKP, int DVP>
 cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4], cudaStream_t st) {
-  const int64_t split = p.tokens / sg.tokens;  // at most that many segments before a last one
+  const int64_t split = split_segments(p, sg.tokens);
   if (split > 0) {
     sg.partial = true;
     const cudaError_t e = launch_t<DKP, DVP, false, true>(p, sg, m, split * p.Hv, st);
@@ -1046,14 +1061,29 @@ cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4],
 
 }  // namespace
 
-// Tokens of a segment.
+// Tokens of a segment.  One block an SM walks over a segment, so that n
+// segments of every head take `waves` rounds of n heads / SMs blocks; a round
+// costs its chunks and about two more (its start and its end).  The segments'
+// own states, which a second launch needs first, cost about half of that again:
+// a call is split only where it gains more.  Sequences shorter than a segment
+// stay whole.
 int linear_segment(const LinParams &p) {
-  (void)p;
-  return 1 << 30;
+  constexpr int kSMs = 148;
+  const int64_t chunks = (p.tokens + kC - 1) / kC;
+  int64_t best = chunks, cost = chunks + 2;
+  for (int waves = 1; waves <= 4; ++waves) {
+    const int64_t n = kSMs * waves / p.Hv;
+    if (n < 2) continue;
+    const int64_t each = (chunks + n - 1) / n;
+    const int64_t c = waves * (each + 2) * 3 / 2;
+    if (c < cost) best = each, cost = c;
+  }
+  return static_cast<int>(best < 1 ? 1 : best) * kC;
 }
 
 size_t linear_chunks_workspace(const LinParams &p) {
-  const int64_t entries = 2 * static_cast<int64_t>(p.tokens / linear_segment(p));
+  // a sequence of s > 1 segments needs s entries
+  const int64_t entries = 2 * split_segments(p, linear_segment(p));
   return static_cast<size_t>(entries * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
 }
 
@@ -1074,7 +1104,7 @@ cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream
   sg.tokens = linear_segment(p);
   sg.partial = false;
   sg.states = static_cast<float *>(workspace);
-  sg.decays = sg.states + 2 * static_cast<int64_t>(p.tokens / sg.tokens) * p.Hv * p.dk * p.dv;
+  sg.decays = sg.states + 2 * split_segments(p, sg.tokens) * p.Hv * p.dk * p.dv;
   if (p.dk <= 64) return p.dv <= 64 ? launch_d<64, 64>(p, sg, m, st) : launch_d<64, 128>(p, sg, m, st);
   return p.dv <= 64 ? launch_d<128, 64>(p, sg, m, st) : launch_d<128, 128>(p, sg, m, st);
 }

@@ -17,31 +17,41 @@ namespace {
 constexpr int kNT = 256;
 constexpr unsigned kAllLanes = 0xffffffffu;
 
-__device__ __forceinline__ float activate(int act, float x) {
-  if (act == 0) return x;
-  const float s = __fdividef(1.0f, 1.0f + expf(-x));
-  return act == 1 ? x * s : s;
-}
-
-// Sum over the `lanes` lanes (a power of two) or the block that hold a row.
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float x, int lanes, float *scratch) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(kAllLanes, x, o);
-  if constexpr (BLOCK) {
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0f;
+// The activation of a row's values: one choice for all of them.  The
+// exponential's argument is rounded once, an error of |x| 2^-24 of the result.
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&x)[N]) {
+  if (act == 1) {
 #pragma unroll
-    for (int i = 0; i < kNT / 32; ++i) x += scratch[i];
+    for (int j = 0; j < N; ++j) x[j] = __fdividef(x[j], 1.0f + __expf(-x[j]));
+  } else if (act == 2) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = __fdividef(1.0f, 1.0f + __expf(-x[j]));
   }
-  return x;
 }
 
-// `lanes` threads a row (kNT with BLOCK), CPL chunks of VEC values each.
-// `blocks` is the grid; blocks * (kNT / lanes) % groups == 0 unless every row
-// has threads of its own.
-template <bool BF16, bool OUT16, int VEC, int CPL, bool BLOCK>
+// Sums over the `lanes` lanes (a power of two) or the block that hold a row.
+template <bool BLOCK, int U>
+__device__ __forceinline__ void row_sums(float (&x)[U], int lanes, float *scratch) {
+  for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(kAllLanes, x[u], o);
+  if constexpr (BLOCK) {
+    static_assert(U == 1, "a block holds one row");
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x[0];
+    __syncthreads();
+    x[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNT / 32; ++i) x[0] += scratch[i];
+  }
+}
+
+// `lanes` threads a row (kNT with BLOCK), CPL chunks of VEC values each, U rows
+// at a time, all of their loads in flight.  Rows go round the blocks in steps
+// of gridDim.x * (kNT / lanes), a multiple of `groups` unless every row has
+// threads of its own.
+template <bool BF16, bool OUT16, bool GATE, int VEC, int CPL, bool BLOCK, int U>
 __global__ void __launch_bounds__(kNT) norm_kernel(const NormParams p, int lanes) {
   __shared__ float scratch[kNT / 32];
   const int per = BLOCK ? 1 : kNT / lanes;  // rows of a block at a time
@@ -66,87 +76,129 @@ __global__ void __launch_bounds__(kNT) norm_kernel(const NormParams p, int lanes
     }
   // every lane of a warp takes part in the reductions until its warp is done
   const int64_t base = row - (BLOCK ? 0 : (threadIdx.x & 31) / lanes);
-  for (int64_t first = base; first < rows; first += step, row += step, token += token_step) {
-    const bool live = row < rows;
-    const int64_t xat = token * p.x_stride + static_cast<int64_t>(group) * p.size;
-    const int64_t zat = token * p.gate_stride + static_cast<int64_t>(group) * p.size;
-    Chunk<BF16, VEC> x[CPL], z[CPL];
+  for (int64_t first = base; first < rows;
+       first += U * step, row += U * step, token += U * token_step) {
+    Raw<BF16, VEC> rx[U][CPL], rz[U][CPL];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      const int at = (c * width + lane) * VEC;
-      const bool in = live && at < p.size;
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = token + u * token_step;
+      const int64_t at0 = static_cast<int64_t>(group) * p.size + lane * VEC;
+      const int64_t xat = t * p.x_stride + at0, zat = t * p.gate_stride + at0;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[c].x[j] = z[c].x[j] = 0.0f;
-      if (in) {
-        x[c].load(p.x, xat + at);
-        if (p.gate) z[c].load(p.gate, zat + at);
-      }
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (p.gate) {
-          z[c].x[j] = activate(p.act, z[c].x[j]);
-          if (p.gate_before) x[c].x[j] *= z[c].x[j];
+      for (int c = 0; c < CPL; ++c) {
+        rx[u][c] = {};
+        if (GATE) rz[u][c] = {};
+        if (row + u * step < rows && (c * width + lane) * VEC < p.size) {
+          rx[u][c].load(p.x, xat + c * width * VEC);
+          if (GATE) rz[u][c].load(p.gate, zat + c * width * VEC);
         }
-        sum += x[c].x[j];
-      }
-    const float mean = p.kind == 1 ? row_sum<BLOCK>(sum, BLOCK ? 32 : lanes, scratch) * inv : 0.0f;
-    float sq = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      if ((c * width + lane) * VEC >= p.size) continue;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        x[c].x[j] -= mean;
-        sq = fmaf(x[c].x[j], x[c].x[j], sq);
       }
     }
-    const float var = row_sum<BLOCK>(sq, BLOCK ? 32 : lanes, scratch) * inv;
-    const float scale = rsqrtf(var + p.eps);
-    const int64_t oat = token * p.out_stride + static_cast<int64_t>(group) * p.size;
+    Chunk<BF16, VEC> x[U][CPL];
+    float sum[U], sq[U];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      const int at = (c * width + lane) * VEC;
+    for (int u = 0; u < U; ++u) {
+      sum[u] = sq[u] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float y = fmaf(x[c].x[j] * scale, w[c][j], bias[c][j]);
-        x[c].x[j] = p.gate == nullptr ? activate(p.act, y) : p.gate_before ? y : y * z[c].x[j];
+      for (int c = 0; c < CPL; ++c) {
+        x[u][c].set(rx[u][c]);
+        if (GATE && p.gate_before) {
+          Chunk<BF16, VEC> z;
+          z.set(rz[u][c]);
+          activate(p.act, z.x);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[u][c].x[j] *= z.x[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum[u] += x[u][c].x[j];
       }
-      if (live && at < p.size) x[c].template store_as<OUT16>(p.out, oat + at);
+    }
+    if (p.kind == 1) {
+      row_sums<BLOCK, U>(sum, BLOCK ? 32 : lanes, scratch);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          const float mean = (c * width + lane) * VEC < p.size ? sum[u] * inv : 0.0f;
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[u][c].x[j] -= mean;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < CPL; ++c)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sq[u] = fmaf(x[u][c].x[j], x[u][c].x[j], sq[u]);
+    row_sums<BLOCK, U>(sq, BLOCK ? 32 : lanes, scratch);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float scale = rsqrtf(fmaf(sq[u], inv, p.eps));
+      const int64_t oat = (token + u * token_step) * p.out_stride +
+                          static_cast<int64_t>(group) * p.size + lane * VEC;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          x[u][c].x[j] = fmaf(x[u][c].x[j] * scale, w[c][j], bias[c][j]);
+        if (!GATE) {
+          activate(p.act, x[u][c].x);
+        } else if (!p.gate_before) {
+          Chunk<BF16, VEC> z;
+          z.set(rz[u][c]);
+          activate(p.act, z.x);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[u][c].x[j] *= z.x[j];
+        }
+        if (row + u * step < rows && (c * width + lane) * VEC < p.size)
+          x[u][c].template store_as<OUT16>(p.out, oat + c * width * VEC);
+      }
     }
   }
 }
 
+template <bool BF16, bool OUT16, int VEC, int CPL, bool BLOCK, int U>
+cudaError_t norm_u(const NormParams &p, int lanes, int64_t grid, cudaStream_t st) {
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const unsigned g = static_cast<unsigned>(grid);
+  if (p.gate != nullptr)
+    norm_kernel<BF16, OUT16, true, VEC, CPL, BLOCK, U><<<g, kNT, 0, st>>>(p, lanes);
+  else
+    norm_kernel<BF16, OUT16, false, VEC, CPL, BLOCK, U><<<g, kNT, 0, st>>>(p, lanes);
+  return cudaGetLastError();
+}
+
+// One row a thread group where the rows do not fill the GPU; else several in
+// flight, from blocks that all run at once (a quarter of the registers for
+// each) and keep every lane on one group: a grid that is a multiple of
+// groups / gcd(groups, rows of a block).
 template <bool BF16, bool OUT16, int VEC, int CPL, bool BLOCK>
 cudaError_t norm_t(const NormParams &p, int lanes, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.groups;
   const int64_t per = BLOCK ? 1 : kNT / lanes;
   const int64_t all = (rows + per - 1) / per;
-  // blocks that keep a lane on one group: a multiple of groups / gcd(groups, per)
   int64_t unit = p.groups;
   for (int64_t g = per; unit % 2 == 0 && g > 1; g /= 2) unit /= 2;
-  const int64_t want = 148 * 16;
-  int64_t grid = all;
-  if (all > want && unit <= want) grid = want / unit * unit;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  norm_kernel<BF16, OUT16, VEC, CPL, BLOCK>
-      <<<static_cast<unsigned>(grid), kNT, 0, st>>>(p, lanes);
-  return cudaGetLastError();
+  constexpr int kMost = BLOCK || CPL * VEC > 16 ? 1 : CPL * VEC > 8 ? 2 : 4;
+  const int64_t want = 148 * 4;
+  if (all <= want * kMost / 2 || unit > want)
+    return norm_u<BF16, OUT16, VEC, CPL, BLOCK, 1>(p, lanes, all, st);
+  return norm_u<BF16, OUT16, VEC, CPL, BLOCK, kMost>(p, lanes, want / unit * unit, st);
 }
 
 template <bool BF16, bool OUT16, int VEC>
 cudaError_t norm_v(const NormParams &p, cudaStream_t st) {
+  // Lanes of a row: 8 values a lane or so, which the reductions are shared by,
+  // up to a warp; then up to kMost chunks a lane; then a block.
   const int chunks = (p.size + VEC - 1) / VEC;
-  constexpr int kMost = VEC == 1 ? 16 : 4;  // chunks of a lane within a warp
+  constexpr int kMost = VEC == 1 ? 16 : 4, kFew = VEC >= 8 ? 1 : VEC == 4 ? 2 : 8;
   if (chunks > 32 * kMost) return norm_t<BF16, OUT16, VEC, 8192 / kNT / VEC, true>(p, kNT, st);
   int lanes = 1;
-  while (lanes < 32 && lanes < chunks) lanes *= 2;
+  while (lanes < 32 && lanes * kFew < chunks) lanes *= 2;
   const int cpl = (chunks + lanes - 1) / lanes;
-  if (cpl <= 1) return norm_t<BF16, OUT16, VEC, 1, false>(p, lanes, st);
-  if (cpl <= kMost / 2) return norm_t<BF16, OUT16, VEC, kMost / 2, false>(p, lanes, st);
+  if (cpl <= kFew) return norm_t<BF16, OUT16, VEC, kFew, false>(p, lanes, st);
+  if (cpl <= kMost / 2 && kMost / 2 > kFew)
+    return norm_t<BF16, OUT16, VEC, kMost / 2, false>(p, lanes, st);
   return norm_t<BF16, OUT16, VEC, kMost, false>(p, lanes, st);
 }
 

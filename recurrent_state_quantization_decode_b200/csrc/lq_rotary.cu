@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kMaxTok = 8;  // tokens of a block
+constexpr int kU = 4;       // heads a thread has in flight
 
 // A head is split into `turned` work items (a pair of chunks in the half
 // layout, one chunk of pairs interleaved) and the chunks behind rot.
@@ -41,60 +42,70 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
   __syncthreads();
   const int turned = INTER ? p.rot / W : half / VEC;
   const int items = turned + (p.d - p.rot) / VEC;
-  // rows (token, head) over threadIdx.y and the grid's second axis
-  for (int r = blockIdx.y * blockDim.y + threadIdx.y; r < nt * heads; r += gridDim.y * blockDim.y) {
-    const int t = r / heads, hh = r - t * heads;
-    const bool is_q = hh < p.Hq;
-    const int head = is_q ? hh : hh - p.Hq;
-    const void *src = is_q ? p.q : p.k;
-    void *dst = is_q ? p.q_out : p.k_out;
-    const int64_t from = (t0 + t) * (is_q ? p.q_stride : p.k_stride) + head * p.d;
-    const int64_t to = (t0 + t) * (is_q ? p.q_out_stride : p.k_out_stride) + head * p.d;
+  const int step = gridDim.y * blockDim.y;
+  for (int t = 0; t < nt; ++t) {
     const float2 *row = cs + t * half;
-    for (int c = threadIdx.x; c < items; c += blockDim.x) {
-      if (c >= turned) {
-        if (is_q ? copy_q : copy_k) {
-          Chunk<BF16, VEC> x;
-          const int at = p.rot + (c - turned) * VEC;
-          x.load(src, from + at);
-          x.store(dst, to + at);
-        }
-      } else if constexpr (!INTER) {
-        Chunk<BF16, VEC> a, b;
-        const int at = c * VEC;
-        a.load(src, from + at);
-        b.load(src, from + half + at);
+    // kU heads at a time, all of their loads in flight
+    for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < heads; h0 += kU * step) {
+      for (int c = threadIdx.x; c < items; c += blockDim.x) {
+        // a: the item's first chunk (the pairs, or a copied chunk); b: the
+        // chunk that a pairs with in the half layout
+        constexpr bool kTwo = !INTER || VEC == 1;
+        const bool turn = c < turned;
+        const int at = turn ? c * W : p.rot + (c - turned) * VEC;
+        const int other = at + (INTER ? 1 : half);
+        Raw<BF16, VEC> ra[kU], rb[kTwo ? kU : 1];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float2 w = row[at + j];
-          const float x = a.x[j], y = b.x[j];
-          a.x[j] = x * w.x - y * w.y;
-          b.x[j] = y * w.x + x * w.y;
+        for (int u = 0; u < kU; ++u) {
+          const int hh = h0 + u * step;
+          const bool is_q = hh < p.Hq;
+          if (hh < heads) {
+            const void *src = is_q ? p.q : p.k;
+            const int64_t from = (t0 + t) * (is_q ? p.q_stride : p.k_stride) +
+                                 (is_q ? hh : hh - p.Hq) * p.d;
+            ra[u].load(src, from + at);
+            if constexpr (kTwo) {
+              if (turn) rb[u].load(src, from + other);
+            }
+          }
         }
-        a.store(dst, to + at);
-        b.store(dst, to + half + at);
-      } else if constexpr (VEC == 1) {
-        Chunk<BF16, 1> a, b;
-        a.load(src, from + 2 * c);
-        b.load(src, from + 2 * c + 1);
-        const float2 w = row[c];
-        const float x = a.x[0], y = b.x[0];
-        a.x[0] = x * w.x - y * w.y;
-        b.x[0] = y * w.x + x * w.y;
-        a.store(dst, to + 2 * c);
-        b.store(dst, to + 2 * c + 1);
-      } else {
-        Chunk<BF16, VEC> a;
-        const int at = c * VEC;
-        a.load(src, from + at);
+        constexpr int kPairs = kTwo ? VEC : VEC / 2;
+        float2 w[kPairs];
+        if (turn) {
 #pragma unroll
-        for (int j = 0; j < VEC / 2; ++j) {
-          const float2 w = row[at / 2 + j];
-          const float x = a.x[2 * j], y = a.x[2 * j + 1];
-          a.x[2 * j] = x * w.x - y * w.y;
-          a.x[2 * j + 1] = y * w.x + x * w.y;
+          for (int j = 0; j < kPairs; ++j) w[j] = row[c * kPairs + j];
         }
-        a.store(dst, to + at);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int hh = h0 + u * step;
+          const bool is_q = hh < p.Hq;
+          if (hh >= heads) break;
+          void *dst = is_q ? p.q_out : p.k_out;
+          const int64_t to = (t0 + t) * (is_q ? p.q_out_stride : p.k_out_stride) +
+                             (is_q ? hh : hh - p.Hq) * p.d;
+          Chunk<BF16, VEC> a, b;
+          a.set(ra[u]);
+          if (turn) {
+            if constexpr (kTwo) {
+              b.set(rb[u]);
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) {
+                const float x = a.x[j], y = b.x[j];
+                a.x[j] = x * w[j].x - y * w[j].y;
+                b.x[j] = y * w[j].x + x * w[j].y;
+              }
+              b.store(dst, to + other);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kPairs; ++j) {
+                const float x = a.x[2 * j], y = a.x[2 * j + 1];
+                a.x[2 * j] = x * w[j].x - y * w[j].y;
+                a.x[2 * j + 1] = y * w[j].x + x * w[j].y;
+              }
+            }
+          }
+          if (turn || (is_q ? copy_q : copy_k)) a.store(dst, to + at);
+        }
       }
     }
   }
@@ -113,9 +124,8 @@ cudaError_t rotary_t(const RotaryParams &p, cudaStream_t st) {
   int tok = 1;
   while (tok < kMaxTok && 2 * tok * half <= kNT && p.tokens / (2 * tok) >= 592) tok *= 2;
   const int gx = (p.tokens + tok - 1) / tok;
-  const int rows = (tok * heads + block.y - 1) / block.y;
   int gy = 1;
-  while (gy < rows && gx * gy < 296) gy *= 2;
+  while (gy * static_cast<int>(block.y) < heads && gx * gy < 296) gy *= 2;
   rotary_kernel<BF16, INTER, VEC><<<dim3(gx, gy), block, tok * half * sizeof(float2), st>>>(
       p, tok, p.q != p.q_out, p.k != p.k_out);
   return cudaGetLastError();
