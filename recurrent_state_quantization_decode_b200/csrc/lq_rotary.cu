@@ -15,17 +15,21 @@
 namespace lq {
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kNT = 128;
 constexpr int kMaxTok = 8;  // tokens of a block
-constexpr int kU = 4;       // heads a thread has in flight
 
-// A head is split into `turned` work items (a pair of chunks in the half
-// layout, one chunk of pairs interleaved) and the chunks behind rot.
+// A head is split into work items: `turned` ones (two chunks that pair up in
+// the half layout, one chunk of pairs interleaved), then those that copy the
+// channels behind rot (as many chunks an item, so that a warp's lanes all do
+// the same).  A thread has kHeads heads in flight: 16,381 tokens x 64 heads x
+// 128, bf16, half layout 88 us with two and 101 with four; interleaved, with
+// half the loads a head, 98 and 89.
 template <bool BF16, bool INTER, int VEC>
-__global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int tok, bool copy_q,
-                                                     bool copy_k) {
-  // the interleaved scalar form takes a pair at a time
-  constexpr int W = INTER && VEC == 1 ? 2 : VEC;
+__global__ void __launch_bounds__(kNT, 8)
+    rotary_kernel(const RotaryParams p, int tok, bool copy_q, bool copy_k) {
+  constexpr bool kTwo = !INTER || VEC == 1;  // two chunks an item
+  constexpr int kHeads = kTwo ? 2 : 4;
+  constexpr int kPairs = kTwo ? VEC : VEC / 2;
   extern __shared__ float2 cs[];  // [tok][rot / 2] (cos, sin)
   const int half = p.rot / 2, heads = p.Hq + p.Hk;
   const int t0 = blockIdx.x * tok, nt = min(tok, p.tokens - t0);
@@ -40,23 +44,22 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
     cs[i] = make_float2(c * p.cos_mul, s * p.sin_mul);
   }
   __syncthreads();
-  const int turned = INTER ? p.rot / W : half / VEC;
-  const int items = turned + (p.d - p.rot) / VEC;
+  const int turned = half / kPairs;
+  const int copied = copy_q || copy_k ? (p.d - p.rot) / VEC : 0;
+  const int items = turned + (kTwo ? (copied + 1) / 2 : copied);
   const int step = gridDim.y * blockDim.y;
   for (int t = 0; t < nt; ++t) {
     const float2 *row = cs + t * half;
-    // kU heads at a time, all of their loads in flight
-    for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < heads; h0 += kU * step) {
+    for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < heads; h0 += kHeads * step) {
       for (int c = threadIdx.x; c < items; c += blockDim.x) {
-        // a: the item's first chunk (the pairs, or a copied chunk); b: the
-        // chunk that a pairs with in the half layout
-        constexpr bool kTwo = !INTER || VEC == 1;
         const bool turn = c < turned;
-        const int at = turn ? c * W : p.rot + (c - turned) * VEC;
-        const int other = at + (INTER ? 1 : half);
-        Raw<BF16, VEC> ra[kU], rb[kTwo ? kU : 1];
+        const int k = c - turned;
+        const int at = turn ? (INTER ? 2 * kPairs : VEC) * c : p.rot + (kTwo ? 2 : 1) * VEC * k;
+        const int other = turn ? (INTER ? at + 1 : at + half) : at + VEC;
+        const bool two = kTwo && (turn || 2 * k + 1 < copied);
+        Raw<BF16, VEC> ra[kHeads], rb[kTwo ? kHeads : 1];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < kHeads; ++u) {
           const int hh = h0 + u * step;
           const bool is_q = hh < p.Hq;
           if (hh < heads) {
@@ -65,18 +68,17 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
                                  (is_q ? hh : hh - p.Hq) * p.d;
             ra[u].load(src, from + at);
             if constexpr (kTwo) {
-              if (turn) rb[u].load(src, from + other);
+              if (two) rb[u].load(src, from + other);
             }
           }
         }
-        constexpr int kPairs = kTwo ? VEC : VEC / 2;
         float2 w[kPairs];
         if (turn) {
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) w[j] = row[c * kPairs + j];
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < kHeads; ++u) {
           const int hh = h0 + u * step;
           const bool is_q = hh < p.Hq;
           if (hh >= heads) break;
@@ -85,16 +87,15 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
                              (is_q ? hh : hh - p.Hq) * p.d;
           Chunk<BF16, VEC> a, b;
           a.set(ra[u]);
+          if constexpr (kTwo) b.set(rb[u]);
           if (turn) {
             if constexpr (kTwo) {
-              b.set(rb[u]);
 #pragma unroll
               for (int j = 0; j < VEC; ++j) {
                 const float x = a.x[j], y = b.x[j];
                 a.x[j] = x * w[j].x - y * w[j].y;
                 b.x[j] = y * w[j].x + x * w[j].y;
               }
-              b.store(dst, to + other);
             } else {
 #pragma unroll
               for (int j = 0; j < kPairs; ++j) {
@@ -104,7 +105,12 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
               }
             }
           }
-          if (turn || (is_q ? copy_q : copy_k)) a.store(dst, to + at);
+          if (turn || (is_q ? copy_q : copy_k)) {
+            a.store(dst, to + at);
+            if constexpr (kTwo) {
+              if (two) b.store(dst, to + other);
+            }
+          }
         }
       }
     }
@@ -114,15 +120,15 @@ __global__ void __launch_bounds__(kNT) rotary_kernel(const RotaryParams p, int t
 template <bool BF16, bool INTER, int VEC>
 cudaError_t rotary_t(const RotaryParams &p, cudaStream_t st) {
   const int half = p.rot / 2, heads = p.Hq + p.Hk;
-  const int items = (INTER ? (VEC == 1 ? half : p.rot / VEC) : half / VEC) + (p.d - p.rot) / VEC;
-  int bx = 1;
-  while (bx < items && bx < 128) bx *= 2;
+  const int rest = (p.d - p.rot) / VEC;
+  const int items = INTER && VEC > 1 ? p.rot / VEC + rest : half / VEC + (rest + 1) / 2;
+  const int bx = items < kNT ? items : kNT;
   const dim3 block(bx, kNT / bx);
   // Several tokens share a block where that fills its threads with sines, but
   // only as long as the blocks still fill the GPU twice over; few tokens
   // instead split their heads over more blocks.
   int tok = 1;
-  while (tok < kMaxTok && 2 * tok * half <= kNT && p.tokens / (2 * tok) >= 592) tok *= 2;
+  while (tok < kMaxTok && 2 * tok * half <= 2 * kNT && p.tokens / (2 * tok) >= 1184) tok *= 2;
   const int gx = (p.tokens + tok - 1) / tok;
   int gy = 1;
   while (gy * static_cast<int>(block.y) < heads && gx * gy < 296) gy *= 2;
