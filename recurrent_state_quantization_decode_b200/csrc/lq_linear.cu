@@ -57,90 +57,183 @@ __global__ void __launch_bounds__(kNT) linear_step_kernel(const LinParams p) {
                 p.out_bf16);
 }
 
-// Packed prompts, one token after the other: the state rows stay in registers,
-// kTok tokens of inputs at a time in shared memory.  Exact fp32 recurrence,
-// any type and length.
-constexpr int kTok = 32;
-
-template <int DK>
-struct TokensSmem {
-  alignas(16) float q[kTok][DK];
-  alignas(16) float k[kTok][DK];
-  float v[kTok][kRows];
-  float o[kTok][kRows];
-  float a[kTok];
-};
+// Packed prompts, token by token: the exact fp32 recurrence, any type and
+// length.  The state rows stay in registers; inputs come in stages of kTok
+// tokens, the next stage's copies under way while one is worked on; kGroup
+// tokens' row sums are reduced together, since nothing waits for them.
+//
+// Bound by its instructions: 3 multiply-adds a state value and token, two
+// values an instruction.  What a single long sequence lacks is parallelism:
+// such calls are cut into segments, whose own states a first launch computes
+// (without outputs) and the second one starts from.
+constexpr int kTok = 16, kGroup = 4;
 
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(kNT) linear_tokens_kernel(const LinParams p) {
+struct TokensSmem {
+  static constexpr int E = BF16 ? 2 : 4;  // bytes of a value
+  alignas(16) uint8_t q[2][kTok][DK * E];
+  alignas(16) uint8_t k[2][kTok][DK * E];
+  alignas(16) uint8_t v[2][kTok][kRows * E];
+  float a[2][kTok];
+  int scratch[2 * kNT / 32 + 4];
+};
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+
+template <int DK, bool BF16, bool OUT>
+__global__ void __launch_bounds__(kNT) linear_tokens_kernel(const LinParams p, const Segments sg) {
   using M = RowMap<DK>;
-  __shared__ TokensSmem<DK> sm;
+  constexpr int E = BF16 ? 2 : 4;
+  __shared__ TokensSmem<DK, BF16> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int blocks = p.dv / kRows;
   const int tile = blockIdx.x / blocks, block0 = blockIdx.x % blocks * kRows;
   const int row0 = warp * 8;
-  const int b = tile / p.Hv, h = tile - b * p.Hv, hk = h / (p.Hv / p.Hk);
-  const bool report = blockIdx.x == b * p.Hv * blocks;
-  const int slot = slot_in_range(p, b, report);
-  if (slot < 0) return;
-  if (slot_taken(p, b, slot, report)) return;
-  const Span span = sequence_span(p, b);
-  if (span.count < 0) {
-    if (report && tid == 0) atomicOr(p.err, kErrBadPhase);
-    return;
-  }
-  const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
-  if (span.count == 0 && !fresh) return;
-  float *S = p.S + ((static_cast<int64_t>(slot) * p.Hv + h) * p.dv + block0 + row0) * DK +
-             M::col(lane);
-  float4 s[M::NP];
-#pragma unroll
-  for (int i = 0; i < M::NP; ++i)
-    s[i] = fresh ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                 : *reinterpret_cast<const float4 *>(S + M::row(lane, i) * DK);
-  for (int t0 = 0; t0 < span.count; t0 += kTok) {
-    const int n = min(kTok, span.count - t0);
-    const int64_t first = span.first + t0;
-    for (int i = tid; i < n * (DK / 4); i += kNT) {
-      const int t = i / (DK / 4), c = i % (DK / 4) * 4;
-      *reinterpret_cast<float4 *>(&sm.q[t][c]) =
-          load_four<BF16>(p.q, (first + t) * p.q_stride + hk * DK + c);
-      *reinterpret_cast<float4 *>(&sm.k[t][c]) =
-          load_four<BF16>(p.k, (first + t) * p.k_stride + hk * DK + c);
+  const int h = tile % p.Hv, hk = h / (p.Hv / p.Hk);
+  Work pl;
+  if (!locate<kNT>(p, sg, tile / p.Hv, !sg.partial && h == 0 && block0 == 0, sm.scratch, pl)) return;
+  const int slot = pl.slot;
+  const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
+  if (!OUT && !sg.partial && !last) return;  // no outputs asked for: the last state alone
+  const int64_t begin = pl.first + pl.index * sg.tokens;
+  const int count = min(sg.tokens, pl.length - pl.index * sg.tokens);
+  if (count == 0 && !fresh) return;
+
+  const int stages = (count + kTok - 1) / kTok;
+  auto fetch = [&](int st) {
+    const int n = min(kTok, count - st * kTok), b = st & 1;
+    const int64_t first = begin + st * kTok;
+    constexpr int kU = DK * E / 16, vU = kRows * E / 16;  // 16-byte units of a row
+    const char *q = static_cast<const char *>(p.q), *k = static_cast<const char *>(p.k);
+    const char *v = static_cast<const char *>(p.v);
+    for (int i = tid; i < n * kU; i += kNT) {
+      const int t = i / kU, u = i % kU * 16;
+      copy16(&sm.q[b][t][u], q + ((first + t) * p.q_stride + hk * DK) * E + u);
+      copy16(&sm.k[b][t][u], k + ((first + t) * p.k_stride + hk * DK) * E + u);
     }
-    for (int i = tid; i < n * kRows; i += kNT)
-      sm.v[i / kRows][i % kRows] =
-          load_value<BF16>(p.v, (first + i / kRows) * p.v_stride + h * p.dv + block0 + i % kRows);
-    if (tid < n) sm.a[tid] = p.decay[p.decay_head ? h : (first + tid) * p.Hv + h];
-    __syncthreads();
-#pragma unroll 2
-    for (int t = 0; t < n; ++t) {
-      const float4 q = *reinterpret_cast<const float4 *>(&sm.q[t][M::col(lane)]);
-      const float4 k = *reinterpret_cast<const float4 *>(&sm.k[t][M::col(lane)]);
-      const float a = sm.a[t];
-      float o[M::NP];
+    for (int i = tid; i < n * vU; i += kNT) {
+      const int t = i / vU, u = i % vU * 16;
+      copy16(&sm.v[b][t][u], v + ((first + t) * p.v_stride + h * p.dv + block0) * E + u);
+    }
+    if (tid < n) copy4(&sm.a[b][tid], p.decay + (p.decay_head ? h : (first + tid) * p.Hv + h));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (stages > 0) fetch(0);
+
+  const int64_t tile_size = static_cast<int64_t>(p.dv) * DK;
+  const int64_t at = static_cast<int64_t>(block0 + row0) * DK + M::col(lane);
+  float *S = p.S + (static_cast<int64_t>(slot) * p.Hv + h) * tile_size + at;
+  float *entry = sg.states + (static_cast<int64_t>(pl.entry) * p.Hv + h) * tile_size + at;
+  const int64_t entry_step = static_cast<int64_t>(p.Hv) * tile_size;
+  float2 s[M::NP][2];
+  auto load = [&](const float *src) {
+#pragma unroll
+    for (int i = 0; i < M::NP; ++i) {
+      const float4 x = *reinterpret_cast<const float4 *>(src + M::row(lane, i) * DK);
+      s[i][0] = make_float2(x.x, x.y), s[i][1] = make_float2(x.z, x.w);
+    }
+  };
+  auto store = [&](float *dst) {
+#pragma unroll
+    for (int i = 0; i < M::NP; ++i)
+      *reinterpret_cast<float4 *>(dst + M::row(lane, i) * DK) =
+          make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y);
+  };
+  if (!fresh && sg.partial && pl.index == 0) {
+    // a split sequence's first state moves to the workspace: the last
+    // segment's blocks write the pool while others still need it
+    load(S);
+    store(entry);
+  }
+  if (fresh || sg.partial) {
+#pragma unroll
+    for (int i = 0; i < M::NP; ++i) s[i][0] = s[i][1] = make_float2(0.0f, 0.0f);
+  } else {
+    load(pl.count > 1 ? entry : S);
+  }
+  if (!sg.partial) {
+    for (int r = 0; r < pl.index; ++r) {
+      const float d = sg.decays[static_cast<int64_t>(pl.entry + 1 + r) * p.Hv + h];
+      const float *src = entry + (r + 1) * entry_step;
 #pragma unroll
       for (int i = 0; i < M::NP; ++i) {
-        const float v = sm.v[t][row0 + M::row(lane, i)];
-        s[i].x = fmaf(a, s[i].x, v * k.x);
-        s[i].y = fmaf(a, s[i].y, v * k.y);
-        s[i].z = fmaf(a, s[i].z, v * k.z);
-        s[i].w = fmaf(a, s[i].w, v * k.w);
-        o[i] = fmaf(s[i].x, q.x, fmaf(s[i].y, q.y, fmaf(s[i].z, q.z, s[i].w * q.w)));
+        const float4 x = *reinterpret_cast<const float4 *>(src + M::row(lane, i) * DK);
+        s[i][0] = __ffma2_rn(s[i][0], make_float2(d, d), make_float2(x.x, x.y));
+        s[i][1] = __ffma2_rn(s[i][1], make_float2(d, d), make_float2(x.z, x.w));
       }
-      const float sum = M::reduce(o, lane);
-      if (M::writes(lane)) sm.o[t][row0 + M::reduced_row(lane)] = sum;
     }
-    __syncthreads();
-    if (p.out != nullptr)
-      for (int i = tid; i < n * kRows; i += kNT)
-        store_value(p.out,
-                    ((first + i / kRows) * p.Hv + h) * p.dv + block0 + i % kRows,
-                    sm.o[i / kRows][i % kRows], p.out_bf16);
   }
+
+  double total = 1.0;  // the segment's whole decay
+  for (int st = 0; st < stages; ++st) {
+    const int n = min(kTok, count - st * kTok), b = st & 1;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the stage is in; the other one is free
+    if (st + 1 < stages) fetch(st + 1);
+    if (sg.partial && tid == 0)
+      for (int t = 0; t < n; ++t) total *= sm.a[b][t];
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += kGroup) {
+      float o[kGroup][M::NP];
 #pragma unroll
-  for (int i = 0; i < M::NP; ++i)
-    *reinterpret_cast<float4 *>(S + M::row(lane, i) * DK) = s[i];
+      for (int g = 0; g < kGroup; ++g) {
+        const int t = t0 + g;
+        if (t < n) {
+          const float4 k = load_four<BF16>(sm.k[b][t], M::col(lane));
+          const float4 q = OUT ? load_four<BF16>(sm.q[b][t], M::col(lane)) : k;
+          const float2 k0 = make_float2(k.x, k.y), k1 = make_float2(k.z, k.w);
+          const float2 q0 = make_float2(q.x, q.y), q1 = make_float2(q.z, q.w);
+          const float2 a = make_float2(sm.a[b][t], sm.a[b][t]);
+          float v[M::NP];
+          load_rows<BF16, M::NP>(sm.v[b][t], row0 + M::row(lane, 0), v);
+#pragma unroll
+          for (int i = 0; i < M::NP; ++i) {
+            const float2 vv = make_float2(v[i], v[i]);
+            s[i][0] = __ffma2_rn(a, s[i][0], __fmul2_rn(vv, k0));
+            s[i][1] = __ffma2_rn(a, s[i][1], __fmul2_rn(vv, k1));
+            if (OUT) {
+              const float2 x = __ffma2_rn(s[i][1], q1, __fmul2_rn(s[i][0], q0));
+              o[g][i] = x.x + x.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < M::NP; ++i) o[g][i] = 0.0f;
+        }
+      }
+      if constexpr (OUT) {
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) o[g][0] = M::reduce(o[g], lane);
+        if (M::writes(lane)) {
+          const int64_t row = block0 + row0 + M::reduced_row(lane);
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g)
+            if (t0 + g < n)
+              store_value(p.out, ((begin + st * kTok + t0 + g) * p.Hv + h) * p.dv + row, o[g][0],
+                          p.out_bf16);
+        }
+      }
+    }
+  }
+  if (sg.partial) {
+    store(entry + (pl.index + 1) * entry_step);
+    if (tid == 0 && block0 == 0)
+      sg.decays[static_cast<int64_t>(pl.entry + 1 + pl.index) * p.Hv + h] =
+          static_cast<float>(total);
+  } else if (last) {
+    store(S);
+  }
 }
 
 template <int DK>
@@ -153,14 +246,38 @@ cudaError_t step_d(const LinParams &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int DK>
-cudaError_t tokens_d(const LinParams &p, cudaStream_t st) {
-  const int grid = p.B * p.Hv * (p.dv / kRows);
-  if (p.in_bf16)
-    linear_tokens_kernel<DK, true><<<grid, kNT, 0, st>>>(p);
+// Tokens of a segment: so many that the segments' blocks fill the GPU about
+// once (5 of them an SM), but a launch's worth at least.
+int tokens_segment(const LinParams &p) {
+  constexpr int64_t kBlocks = 148 * 5, kLeast = 64;
+  const int64_t each = static_cast<int64_t>(p.tokens) * p.Hv * (p.dv / kRows) / kBlocks;
+  const int64_t n = (each + kTok - 1) / kTok * kTok;
+  return static_cast<int>(n < kLeast ? kLeast : n);
+}
+
+template <int DK, bool BF16>
+cudaError_t tokens_t(const LinParams &p, Segments sg, cudaStream_t st) {
+  const int64_t split = split_segments(p, sg.tokens), each = static_cast<int64_t>(p.Hv) * (p.dv / kRows);
+  if ((split + p.B) * each > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (split > 0) {
+    sg.partial = true;
+    linear_tokens_kernel<DK, BF16, false>
+        <<<static_cast<unsigned>(split * each), kNT, 0, st>>>(p, sg);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    sg.partial = false;
+  }
+  const unsigned grid = static_cast<unsigned>((split + p.B) * each);
+  if (p.out != nullptr)
+    linear_tokens_kernel<DK, BF16, true><<<grid, kNT, 0, st>>>(p, sg);
   else
-    linear_tokens_kernel<DK, false><<<grid, kNT, 0, st>>>(p);
+    linear_tokens_kernel<DK, BF16, false><<<grid, kNT, 0, st>>>(p, sg);
   return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t tokens_d(const LinParams &p, const Segments &sg, cudaStream_t st) {
+  return p.in_bf16 ? tokens_t<DK, true>(p, sg, st) : tokens_t<DK, false>(p, sg, st);
 }
 
 }  // namespace
@@ -171,10 +288,15 @@ cudaError_t launch_linear_step(const LinParams &p, cudaStream_t st) {
   return step_d<128>(p, st);
 }
 
-cudaError_t launch_linear_tokens(const LinParams &p, cudaStream_t st) {
-  if (p.dk == 32) return tokens_d<32>(p, st);
-  if (p.dk == 64) return tokens_d<64>(p, st);
-  return tokens_d<128>(p, st);
+size_t linear_tokens_workspace(const LinParams &p) {
+  return segments_workspace(p, tokens_segment(p));
+}
+
+cudaError_t launch_linear_tokens(const LinParams &p, void *workspace, cudaStream_t st) {
+  const Segments sg = segments_in(p, tokens_segment(p), workspace);
+  if (p.dk == 32) return tokens_d<32>(p, sg, st);
+  if (p.dk == 64) return tokens_d<64>(p, sg, st);
+  return tokens_d<128>(p, sg, st);
 }
 
 }  // namespace lq

@@ -33,6 +33,21 @@ __device__ __forceinline__ float4 load_four(const void *p, int64_t i) {
   }
 }
 
+// N consecutive values (aligned to their size together, 16 bytes at most).
+template <bool BF16, int N>
+__device__ __forceinline__ void load_rows(const void *p, int i, float (&x)[N]) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 v = load_four<BF16>(p, i + j);
+      x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = load_value<BF16>(p, i + j);
+  }
+}
+
 __device__ __forceinline__ void store_value(void *p, int64_t i, float x, int bf16) {
   if (bf16)
     reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
@@ -74,16 +89,178 @@ __device__ __forceinline__ Span sequence_span(const LinParams &p, int b) {
   return {lo, hi - lo};
 }
 
+struct Segments {
+  int tokens;      // tokens of a segment
+  bool partial;    // segments before a sequence's last: their own state, into the workspace
+  float *states;   // workspace: per split sequence its first state, then each segment's state
+  float *decays;   // workspace: [entry][Hv] the segments' whole decays
+};
+
+// Where a block works.
+struct Place {
+  int b, index, count;  // sequence, its segment, its segments
+  int entry;            // the sequence's first workspace entry
+};
+
+// Segments are numbered through the sequences.  Whole block of NT threads;
+// `scratch` is 2 * NT / 32 + 4 ints of shared memory.  Returns false if there are fewer than `wanted` + 1.
+template <int NT>
+__device__ __forceinline__ bool find_place(const LinParams &p, const Segments &sg, int wanted,
+                                           int *scratch, Place &pl) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int done = 0, entries = 0;
+  int *found = scratch + 2 * (NT / 32);
+  if (threadIdx.x == 0) found[0] = -1;
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    const int b = b0 + threadIdx.x;
+    int segs = 0, cnt = 0, ent = 0;
+    if (b < p.B) {
+      const Span s = sequence_span(p, b);
+      segs = s.count <= 0 ? 1 : (s.count + sg.tokens - 1) / sg.tokens;
+      cnt = sg.partial ? segs - 1 : segs;
+      ent = segs > 1 ? segs : 0;
+    }
+    int c = cnt, e = ent;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int c2 = __shfl_up_sync(kAllLanes, c, o), e2 = __shfl_up_sync(kAllLanes, e, o);
+      if (lane >= o) c += c2, e += e2;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = c, scratch[(NT / 32) + warp] = e;
+    __syncthreads();
+    int before = done, ebefore = entries;
+#pragma unroll
+    for (int w = 0; w < (NT / 32); ++w) {
+      if (w < warp) before += scratch[w], ebefore += scratch[(NT / 32) + w];
+      done += scratch[w], entries += scratch[(NT / 32) + w];
+    }
+    const int first = before + c - cnt;
+    if (wanted >= first && wanted < first + cnt) {
+      found[0] = b;
+      found[1] = wanted - first;
+      found[2] = segs;
+      found[3] = ebefore + e - ent;
+    }
+    if (wanted < done) break;
+  }
+  __syncthreads();
+  pl = {found[0], found[1], found[2], found[3]};
+  return pl.b >= 0;
+}
+
+// What a block works on: a segment of a sequence.
+struct Work {
+  int b, index, count, entry;  // as in Place
+  int slot;
+  int first, length;  // of the sequence's tokens
+  bool fresh;
+};
+
+// Segment `wanted` in the call's order, checked: false if there is none, or if
+// its sequence is left out (no slot, a slot past the pool or an earlier
+// sequence's, offsets that do not ascend).  With `reports`, a fault goes into
+// the error word.  Up to 128 sequences every warp reads them all at once and
+// keeps them in registers, one round trip to L2 in place of four.
+template <int NT>
+__device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, int wanted,
+                                       bool reports, int *scratch, Work &w) {
+  const int lane = threadIdx.x & 31;
+  bool fault = false, taken = false;
+  if (p.B <= 128) {
+    int lo[4], hi[4], slots[4], fresh[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = j * 32 + lane;
+      lo[j] = hi[j] = fresh[j] = 0, slots[j] = -1;
+      if (b < p.B) {
+        lo[j] = p.offsets[b], hi[j] = p.offsets[b + 1];
+        slots[j] = p.slots != nullptr ? p.slots[b] : b;
+        if (p.fresh != nullptr) fresh[j] = p.fresh[b] != 0;
+      }
+    }
+    int done = 0, entries = 0;
+    unsigned hit = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (hit != 0 || j * 32 >= p.B) continue;
+      const int count = lo[j] < 0 || hi[j] < lo[j] || hi[j] > p.tokens ? -1 : hi[j] - lo[j];
+      const int segs = j * 32 + lane >= p.B ? 0 : count <= 0 ? 1 : (count + sg.tokens - 1) / sg.tokens;
+      const int cnt = sg.partial && segs > 0 ? segs - 1 : segs, ent = segs > 1 ? segs : 0;
+      int c = cnt, e = ent;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int c2 = __shfl_up_sync(kAllLanes, c, o), e2 = __shfl_up_sync(kAllLanes, e, o);
+        if (lane >= o) c += c2, e += e2;
+      }
+      const int first = done + c - cnt;
+      hit = __ballot_sync(kAllLanes, wanted >= first && wanted < first + cnt);
+      if (hit != 0) {
+        const int from = __ffs(hit) - 1;
+        w.b = j * 32 + from;
+        w.index = wanted - __shfl_sync(kAllLanes, first, from);
+        w.count = __shfl_sync(kAllLanes, segs, from);
+        w.entry = __shfl_sync(kAllLanes, entries + e - ent, from);
+        w.slot = __shfl_sync(kAllLanes, slots[j], from);
+        w.first = __shfl_sync(kAllLanes, lo[j], from);
+        w.length = __shfl_sync(kAllLanes, count, from);
+        w.fresh = __shfl_sync(kAllLanes, fresh[j], from) != 0;
+      }
+      done += __shfl_sync(kAllLanes, c, 31);
+      entries += __shfl_sync(kAllLanes, e, 31);
+    }
+    if (hit == 0) return false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      taken = taken || __any_sync(kAllLanes, j * 32 + lane < w.b && slots[j] == w.slot);
+    taken = taken && p.slots != nullptr;
+    if (w.slot < 0) return false;
+    fault = w.slot >= p.num_slots || taken || w.length < 0;
+  } else {
+    Place pl;
+    if (!find_place<NT>(p, sg, wanted, scratch, pl)) return false;
+    w.b = pl.b, w.index = pl.index, w.count = pl.count, w.entry = pl.entry;
+    w.slot = p.slots != nullptr ? p.slots[w.b] : w.b;
+    const Span s = sequence_span(p, w.b);
+    w.first = s.first, w.length = s.count;
+    w.fresh = p.fresh != nullptr && p.fresh[w.b] != 0;
+    if (w.slot < 0) return false;
+    int same = 0;
+    if (p.slots != nullptr)
+      for (int i = threadIdx.x; i < w.b; i += NT) same |= p.slots[i] == w.slot;
+    taken = __syncthreads_or(same) != 0;
+    fault = w.slot >= p.num_slots || taken || w.length < 0;
+  }
+  if (fault && reports && w.index == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadPhase);
+  return !fault;
+}
+
+// At most how many segments come before a sequence's last one.
+inline int64_t split_segments(const LinParams &p, int segment) {
+  return p.tokens > segment ? p.tokens / segment : 0;
+}
+
+// Workspace of a call in segments: a sequence of s > 1 of them needs s entries,
+// a state and a decay each for every value head.
+inline size_t segments_workspace(const LinParams &p, int segment) {
+  const int64_t entries = 2 * split_segments(p, segment);
+  return static_cast<size_t>(entries * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
+}
+inline Segments segments_in(const LinParams &p, int segment, void *workspace) {
+  float *states = static_cast<float *>(workspace);
+  return {segment, false, states,
+          states + 2 * split_segments(p, segment) * p.Hv * p.dk * p.dv};
+}
+
 // A warp's share of state rows: 8 rows of DK columns, 4 columns a lane, LPR
-// lanes a row and NP passes.  Sums over a row leave pass (lane % LPR) / 4 of
-// the lane's row group in every lane.
+// lanes a row, NP consecutive rows a lane.  Sums over a row leave that of row
+// (lane % LPR) / 4 of its rows in every lane.
 template <int DK>
 struct RowMap {
   static constexpr int LPR = DK / 4;
-  static constexpr int RPP = 32 / LPR;  // rows a pass
-  static constexpr int NP = 8 / RPP;
+  static constexpr int NP = LPR / 4;
   static __device__ __forceinline__ int col(int lane) { return lane % LPR * 4; }
-  static __device__ __forceinline__ int row(int lane, int pass) { return pass * RPP + lane / LPR; }
+  static __device__ __forceinline__ int row(int lane, int i) { return lane / LPR * NP + i; }
   // NP row sums over LPR lanes, halving the values a lane holds at each step
   // while there are any: NP - 1 + 2 shuffles instead of NP log2(LPR).
   static __device__ __forceinline__ float reduce(float (&x)[NP], int lane) {

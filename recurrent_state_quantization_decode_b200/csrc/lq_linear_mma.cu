@@ -51,67 +51,7 @@ namespace {
 
 constexpr int kC = 128;        // tokens of a chunk
 constexpr int kNT = 768;
-constexpr int kWarps = kNT / 32;
 constexpr uint32_t kPolls = 1u << 18;  // of 64 polls each
-
-struct Segments {
-  int tokens;      // tokens of a segment, a multiple of kC
-  bool partial;    // segments before a sequence's last: their own state, into the workspace
-  float *states;   // workspace: per split sequence its first state, then each segment's state
-  float *decays;   // workspace: [entry][Hv] the segments' whole decays
-};
-
-// Where a block works.
-struct Place {
-  int b, index, count;  // sequence, its segment, its segments
-  int entry;            // the sequence's first workspace entry
-};
-
-// Segments are numbered through the sequences.  Whole block; `scratch` is
-// 2 * kWarps + 4 ints.  Returns false if there are fewer than `wanted` + 1.
-__device__ __forceinline__ bool find_place(const LinParams &p, const Segments &sg, int wanted,
-                                           int *scratch, Place &pl) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int done = 0, entries = 0;
-  int *found = scratch + 2 * kWarps;
-  if (threadIdx.x == 0) found[0] = -1;
-  for (int b0 = 0; b0 < p.B; b0 += kNT) {
-    const int b = b0 + threadIdx.x;
-    int segs = 0, cnt = 0, ent = 0;
-    if (b < p.B) {
-      const Span s = sequence_span(p, b);
-      segs = s.count <= 0 ? 1 : (s.count + sg.tokens - 1) / sg.tokens;
-      cnt = sg.partial ? segs - 1 : segs;
-      ent = segs > 1 ? segs : 0;
-    }
-    int c = cnt, e = ent;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int c2 = __shfl_up_sync(kAllLanes, c, o), e2 = __shfl_up_sync(kAllLanes, e, o);
-      if (lane >= o) c += c2, e += e2;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = c, scratch[kWarps + warp] = e;
-    __syncthreads();
-    int before = done, ebefore = entries;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += scratch[w], ebefore += scratch[kWarps + w];
-      done += scratch[w], entries += scratch[kWarps + w];
-    }
-    const int first = before + c - cnt;
-    if (wanted >= first && wanted < first + cnt) {
-      found[0] = b;
-      found[1] = wanted - first;
-      found[2] = segs;
-      found[3] = ebefore + e - ent;
-    }
-    if (wanted < done) break;
-  }
-  __syncthreads();
-  pl = {found[0], found[1], found[2], found[3]};
-  return pl.b >= 0;
-}
 
 struct Decays {
   float a[kC];     // the tokens' decays, 1 behind the last token
@@ -177,14 +117,6 @@ __device__ __forceinline__ void store_shared16(uint32_t addr, uint32_t a, uint32
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
-}
-__device__ __forceinline__ uint4 load_shared16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 // v[at ..] to 32 aligned bytes.
 __device__ __forceinline__ void store_global32(void *p, const uint32_t (&v)[16], int at) {
@@ -294,22 +226,15 @@ __global__ void __launch_bounds__(kNT, 1)
   Control &ctl = *reinterpret_cast<Control *>(smem + T::kControl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
-  Place pl;
-  if (!find_place(p, sg, blockIdx.x / p.Hv, reinterpret_cast<int *>(smem), pl)) return;
-  const bool report = !sg.partial && pl.index == 0 && h == 0;
-  const int slot = slot_in_range(p, pl.b, report);
-  if (slot < 0) return;
-  if (slot_taken(p, pl.b, slot, report)) return;
-  const Span span = sequence_span(p, pl.b);
-  if (span.count < 0) {
-    if (report && tid == 0) atomicOr(p.err, kErrBadPhase);
+  Work pl;
+  if (!locate<kNT>(p, sg, blockIdx.x / p.Hv, !sg.partial && h == 0, reinterpret_cast<int *>(smem),
+                   pl))
     return;
-  }
-  const bool last = pl.index == pl.count - 1;
+  const int slot = pl.slot;
+  const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
   if (STATES && !sg.partial && !last) return;  // no outputs asked for: the last state alone
-  const bool fresh = p.fresh != nullptr && p.fresh[pl.b] != 0;
-  const int first = span.first + pl.index * sg.tokens;
-  const int n = min(sg.tokens, span.count - pl.index * sg.tokens);
+  const int first = pl.first + pl.index * sg.tokens;
+  const int n = min(sg.tokens, pl.length - pl.index * sg.tokens);
   const int chunks = (n + kC - 1) / kC;
   if (chunks == 0 && !fresh) return;
   const int64_t tile = static_cast<int64_t>(p.dv) * p.dk;
@@ -321,7 +246,7 @@ __global__ void __launch_bounds__(kNT, 1)
   volatile int *dead = &ctl.dead;
   const uint32_t bars = base + T::kControl + static_cast<uint32_t>(offsetof(Control, bar));
   auto at = [bars](uint32_t barrier) { return bars + 8 * barrier; };
-  __syncthreads();  // the scratch of find_place is read
+  __syncthreads();  // what locate left in shared memory is read
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       tc::bar_init(at(kFullQK + s), 1);
@@ -359,6 +284,12 @@ __global__ void __launch_bounds__(kNT, 1)
   const uint32_t tm = ctl.tmem;
   const bool sound = ctl.dead == 0;
 
+  // Whether a chunk's outputs go through shared memory and a bulk store: whole
+  // chunks do (the rows behind a last one are another sequence's), where the
+  // outputs are aligned for it.
+  auto staged = [&](int c) {
+    return !F32OUT && n - c * kC >= kC && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  };
   if (!sound) {
   } else if (warp >= 20) {
     set_registers_down<64>();
@@ -536,43 +467,18 @@ __global__ void __launch_bounds__(kNT, 1)
         ok = decays(0);
       }
       if (ok && chunks > 1) ok = decays(1);
-      const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 #pragma unroll 1
       for (int c = 0; ok && c < chunks; ++c) {
         if constexpr (!STATES && !F32OUT) {
-          // the chunk's outputs
-          const int s = c & 1, live = min(kC, n - c * kC);
-          const uint32_t from = base + (T::kOverQ ? s * T::kStage : T::kOut);
+          // the chunk's outputs, unless they have left from registers
+          const int s = c & 1;
           if (!(ok = wait_warp(at(kStaged), c & 1, dead, p.err))) break;
-          if (whole && live == kC) {
-            if (lane == 0) {
+          if (lane == 0 && staged(c)) {
+            const uint32_t from = base + (T::kOverQ ? s * T::kStage : T::kOut);
 #pragma unroll
-              for (int x = 0; x < DVP; x += 64)
-                tc::store_tile(&mo, from + x * (2 * kC), x, h, first + c * kC);
-              tc::store_done();
-            }
-          } else {
-            // rows behind the last are another sequence's
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out);
-            const int units = p.dv / 8;
-#pragma unroll 1
-            for (int i = lane; i < live * units; i += 32) {
-              const int row = i / units, u = i % units;
-              const uint4 v = load_shared16(from + u / 8 * (kC * 128) + row * 128 +
-                                            ((u % 8 ^ (row & 7)) << 4));
-              __nv_bfloat16 *to =
-                  dst + (static_cast<int64_t>(first + c * kC + row) * p.Hv + h) * p.dv + u * 8;
-              if (whole) {
-                *reinterpret_cast<uint4 *>(to) = v;
-              } else {
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  reinterpret_cast<uint16_t *>(to)[j] =
-                      static_cast<uint16_t>(x[j / 2] >> (j % 2 * 16));
-              }
-            }
-            tc::fence_async();  // the tile is loaded over next
+            for (int x = 0; x < DVP; x += 64)
+              tc::store_tile(&mo, from + x * (2 * kC), x, h, first + c * kC);
+            tc::store_done();
           }
           arrive_warp(at(kStored));
           if (T::kOverQ) arrive_warp(at(kEmptyQ + s));
@@ -745,17 +651,24 @@ __global__ void __launch_bounds__(kNT, 1)
       const float4 *row = reinterpret_cast<const float4 *>(src + e * p.dk + f0);
 #pragma unroll
       for (int f = 0; f < kF; f += 4) {
-        if (f % 16 == 0) asm volatile("" ::: "memory");  // 16 values in flight
         const float4 x = mine ? row[f / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         S[f] = x.x, S[f + 1] = x.y, S[f + 2] = x.z, S[f + 3] = x.w;
       }
     };
     auto store_state = [&](float *dst) {
-      float4 *row = reinterpret_cast<float4 *>(dst + e * p.dk + f0);
-      if (mine) {
+      float *row = dst + e * p.dk + f0;
+      if (mine && (reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+        for (int f = 0; f < kF; f += 8) {  // whole sectors
+          uint32_t v[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = bits(S[f + j]);
+          store_global32(row + f, v, 0);
+        }
+      } else if (mine) {
 #pragma unroll
         for (int f = 0; f < kF; f += 4)
-          row[f / 4] = make_float4(S[f], S[f + 1], S[f + 2], S[f + 3]);
+          *reinterpret_cast<float4 *>(row + f) = make_float4(S[f], S[f + 1], S[f + 2], S[f + 3]);
       }
     };
     if (!fresh && sg.partial && pl.index == 0) {
@@ -837,62 +750,54 @@ __global__ void __launch_bounds__(kNT, 1)
     auto outputs = [&](int c) {
       if (!wait_warp(at(kOFull), c & 1, dead, p.err)) return false;
       tc::after_sync();
-      if constexpr (!F32OUT) {
-        if (!T::kOverQ && c > 0 && !wait_warp(at(kStored), (c - 1) & 1, dead, p.err)) return false;
-        const uint32_t to = base + (T::kOverQ ? (c & 1) * T::kStage : T::kOut) + row * 128;
+      const bool through = staged(c);
+      if (!F32OUT && !T::kOverQ && c > 0 && !wait_warp(at(kStored), (c - 1) & 1, dead, p.err))
+        return false;
+      const uint32_t to_tile = base + (T::kOverQ ? (c & 1) * T::kStage : T::kOut) + row * 128;
+      const bool live = c * kC + row < n;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+      const int64_t to = (static_cast<int64_t>(first + c * kC + row) * p.Hv + h) * p.dv;
 #pragma unroll 1
-        for (int e = half_e; e < half_e + DVP / 2; e += 32) {
-          uint32_t x[16], y[16];
-          tc::load16(tm + kO + lanes + e, x);
-          tc::load16(tm + kO + lanes + e + 16, y);
-          tc::wait_loads(x, y);
+      for (int e = half_e; e < half_e + DVP / 2; e += 16) {
+        uint32_t x[16];
+        tc::load16(tm + kO + lanes + e, x);
+        tc::wait_loads(x);
+        if constexpr (!F32OUT) {
+          uint32_t v[16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              const uint32_t(&o)[16] = i == 0 ? x : y;
-              const int u = (e + i * 16 + j) % 64 / 8;
-              store_shared16(to + e / 64 * (kC * 128) + ((u ^ (row & 7)) << 4),
-                             pack(floats(o[j], o[j + 1])), pack(floats(o[j + 2], o[j + 3])),
-                             pack(floats(o[j + 4], o[j + 5])), pack(floats(o[j + 6], o[j + 7])));
-            }
-          }
-        }
-        tc::before_sync();
-        arrive_warp(at(kOEmpty));
-        tc::fence_async();
-        arrive_warp(at(kStaged));
-      } else {
-        const bool live = c * kC + row < n;
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        float *to = static_cast<float *>(p.out) +
-                    (static_cast<int64_t>(first + c * kC + row) * p.Hv + h) * p.dv;
-#pragma unroll 1
-        for (int e = half_e; e < half_e + DVP / 2; e += 32) {
-          uint32_t x[16], y[16];
-          tc::load16(tm + kO + lanes + e, x);
-          tc::load16(tm + kO + lanes + e + 16, y);
-          tc::wait_loads(x, y);
-          if (e + 32 == half_e + DVP / 2) {
-            tc::before_sync();
-            arrive_warp(at(kOEmpty));
-          }
-          if (live && e < p.dv) {
+          for (int j = 0; j < 8; ++j) v[j] = pack(floats(x[2 * j], x[2 * j + 1]));
+          if (through) {
+            const int u = e % 64 / 8;
+            const uint32_t block = to_tile + e / 64 * (kC * 128);
+            store_shared16(block + ((u ^ (row & 7)) << 4), v[0], v[1], v[2], v[3]);
+            store_shared16(block + (((u + 1) ^ (row & 7)) << 4), v[4], v[5], v[6], v[7]);
+          } else if (live && e < p.dv) {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + to + e;
             if (wide) {
-              store_global32(to + e, x, 0);
-              store_global32(to + e + 8, x, 8);
-              store_global32(to + e + 16, y, 0);
-              store_global32(to + e + 24, y, 8);
+              store_global32(dst, v, 0);
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                to[e + j] = __uint_as_float(x[j]);
-                to[e + 16 + j] = __uint_as_float(y[j]);
-              }
+              for (int j = 0; j < 16; ++j)
+                reinterpret_cast<uint16_t *>(dst)[j] = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
             }
           }
-          __syncwarp();
+        } else if (live && e < p.dv) {
+          float *dst = static_cast<float *>(p.out) + to + e;
+          if (wide) {
+            store_global32(dst, x, 0);
+            store_global32(dst + 8, x, 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dst[j] = __uint_as_float(x[j]);
+          }
         }
+        __syncwarp();
+      }
+      tc::before_sync();
+      arrive_warp(at(kOEmpty));
+      if constexpr (!F32OUT) {
+        tc::fence_async();
+        arrive_warp(at(kStaged));
       }
       return true;
     };
@@ -1039,11 +944,6 @@ cudaError_t launch_t(const LinParams &p, const Segments &sg, const CUtensorMap (
   return cudaGetLastError();
 }
 
-// At most how many segments come before a sequence's last one.
-int64_t split_segments(const LinParams &p, int segment) {
-  return p.tokens > segment ? p.tokens / segment : 0;
-}
-
 template <int DKP, int DVP>
 cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4], cudaStream_t st) {
   const int64_t split = split_segments(p, sg.tokens);
@@ -1082,9 +982,7 @@ int linear_segment(const LinParams &p) {
 }
 
 size_t linear_chunks_workspace(const LinParams &p) {
-  // a sequence of s > 1 segments needs s entries
-  const int64_t entries = 2 * split_segments(p, linear_segment(p));
-  return static_cast<size_t>(entries * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
+  return segments_workspace(p, linear_segment(p));
 }
 
 cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream_t st) {
@@ -1100,11 +998,7 @@ cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream
         !encode(&m[3], p.out, p.tokens, p.Hv, p.dv, static_cast<int64_t>(p.Hv) * p.dv))
       return cudaErrorInvalidValue;
   }
-  Segments sg;
-  sg.tokens = linear_segment(p);
-  sg.partial = false;
-  sg.states = static_cast<float *>(workspace);
-  sg.decays = sg.states + 2 * split_segments(p, sg.tokens) * p.Hv * p.dk * p.dv;
+  const Segments sg = segments_in(p, linear_segment(p), workspace);
   if (p.dk <= 64) return p.dv <= 64 ? launch_d<64, 64>(p, sg, m, st) : launch_d<64, 128>(p, sg, m, st);
   return p.dv <= 64 ? launch_d<128, 64>(p, sg, m, st) : launch_d<128, 128>(p, sg, m, st);
 }
