@@ -81,8 +81,8 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
 
 /* Packed prompts of any lengths: sequence b owns tokens offsets[b] ..
  * offsets[b+1]-1 of `tokens` rows (offsets: int32 [batch+1], ascending, within
- * [0, tokens]; a sequence whose pair is not is left out and sets
- * LQ_ERR_DEVICE_BOUNDS).  Runs the recurrence over each sequence from the
+ * [0, tokens]; a sequence whose pair is not, and every one behind a pair that
+ * descends, is left out and sets LQ_ERR_DEVICE_BOUNDS).  Runs the recurrence over each sequence from the
  * state in its slot, or from zeros where fresh[b] != 0 (fresh: nullable int32
  * [batch]), writes out [tokens][Hv][dv] (nullable: states only) and leaves the
  * last state in the slot.  An empty sequence leaves its state, or zeros if

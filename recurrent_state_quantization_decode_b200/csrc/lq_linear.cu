@@ -75,7 +75,7 @@ struct TokensSmem {
   alignas(16) uint8_t k[2][kTok][DK * E];
   alignas(16) uint8_t v[2][kTok][kRows * E];
   float a[2][kTok];
-  int scratch[2 * kNT / 32 + 4];
+  int scratch[kPlaceInts<kNT>];
 };
 
 __device__ __forceinline__ void copy16(void *dst, const void *src) {

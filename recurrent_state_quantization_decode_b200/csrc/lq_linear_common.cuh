@@ -100,23 +100,36 @@ struct Segments {
 struct Place {
   int b, index, count;  // sequence, its segment, its segments
   int entry;            // the sequence's first workspace entry
+  int length;           // its tokens, -1 if it is left out
 };
 
+// From the first pair of offsets that descends, sequences could overlap and so
+// need more workspace than the call has: that one and all behind it are left
+// out, as one segment each.  Then the others' tokens are disjoint, and
+// ceil(n / tokens) <= 2 n / tokens for n >= tokens keeps to the workspace.
+constexpr int kNoDescent = 0x7fffffff;
+template <int NT>
+constexpr int kPlaceInts = 2 * (NT / 32) + 6;
+
 // Segments are numbered through the sequences.  Whole block of NT threads;
-// `scratch` is 2 * NT / 32 + 4 ints of shared memory.  Returns false if there are fewer than `wanted` + 1.
+// `scratch` is kPlaceInts<NT> ints of shared memory.  Returns false if there
+// are fewer than `wanted` + 1.
 template <int NT>
 __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &sg, int wanted,
                                            int *scratch, Place &pl) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int done = 0, entries = 0;
   int *found = scratch + 2 * (NT / 32);
-  if (threadIdx.x == 0) found[0] = -1;
+  if (threadIdx.x == 0) found[0] = -1, found[5] = kNoDescent;
+  __syncthreads();
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + threadIdx.x;
     int segs = 0, cnt = 0, ent = 0;
+    if (b < p.B && p.offsets[b + 1] < p.offsets[b]) atomicMin(&found[5], b);
+    __syncthreads();
+    const int length = b < p.B && b < found[5] ? sequence_span(p, b).count : -1;
     if (b < p.B) {
-      const Span s = sequence_span(p, b);
-      segs = s.count <= 0 ? 1 : (s.count + sg.tokens - 1) / sg.tokens;
+      segs = length <= 0 ? 1 : (length + sg.tokens - 1) / sg.tokens;
       cnt = sg.partial ? segs - 1 : segs;
       ent = segs > 1 ? segs : 0;
     }
@@ -141,11 +154,12 @@ __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &s
       found[1] = wanted - first;
       found[2] = segs;
       found[3] = ebefore + e - ent;
+      found[4] = length;
     }
     if (wanted < done) break;
   }
   __syncthreads();
-  pl = {found[0], found[1], found[2], found[3]};
+  pl = {found[0], found[1], found[2], found[3], found[4]};
   return pl.b >= 0;
 }
 
@@ -179,12 +193,15 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
         if (p.fresh != nullptr) fresh[j] = p.fresh[b] != 0;
       }
     }
-    int done = 0, entries = 0;
+    int done = 0, entries = 0, descent = kNoDescent;
     unsigned hit = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (hit != 0 || j * 32 >= p.B) continue;
-      const int count = lo[j] < 0 || hi[j] < lo[j] || hi[j] > p.tokens ? -1 : hi[j] - lo[j];
+      const unsigned descends = __ballot_sync(kAllLanes, hi[j] < lo[j]);
+      if (descends != 0 && descent == kNoDescent) descent = j * 32 + __ffs(descends) - 1;
+      const bool bad = j * 32 + lane >= descent || lo[j] < 0 || hi[j] > p.tokens;
+      const int count = bad ? -1 : hi[j] - lo[j];
       const int segs = j * 32 + lane >= p.B ? 0 : count <= 0 ? 1 : (count + sg.tokens - 1) / sg.tokens;
       const int cnt = sg.partial && segs > 0 ? segs - 1 : segs, ent = segs > 1 ? segs : 0;
       int c = cnt, e = ent;
@@ -221,8 +238,7 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
     if (!find_place<NT>(p, sg, wanted, scratch, pl)) return false;
     w.b = pl.b, w.index = pl.index, w.count = pl.count, w.entry = pl.entry;
     w.slot = p.slots != nullptr ? p.slots[w.b] : w.b;
-    const Span s = sequence_span(p, w.b);
-    w.first = s.first, w.length = s.count;
+    w.first = p.offsets[w.b], w.length = pl.length;
     w.fresh = p.fresh != nullptr && p.fresh[w.b] != 0;
     if (w.slot < 0) return false;
     int same = 0;

@@ -220,6 +220,9 @@ PROMPTS = {
     "bf16_k128_v32": dict(lengths=[1, 200], hk=5, hv=5, dk=128, dv=32),
     "bf16_one_token": dict(lengths=[1], hk=4, hv=8, dk=128, dv=128),
     "bf16_head_decay": dict(lengths=[700, 90], hk=4, hv=8, dk=128, dv=128, decay="head", out=F32),
+    "bf16_many": dict(lengths=[37 * i % 400 for i in range(60)], hk=4, hv=8, dk=128, dv=128),
+    "bf16_many_f32_out": dict(lengths=[53 * i % 300 for i in range(150)], hk=1, hv=3, dk=64, dv=128, out=F32),
+    "f32_many": dict(lengths=[29 * i % 200 for i in range(140)], hk=1, hv=2, dk=32, dv=64, io=F32, out=F32),
     "bf16_long": dict(lengths=[3001], hk=2, hv=2, dk=128, dv=128, decay="head"),
     "bf16_long_f32_out": dict(lengths=[40, 2500], hk=1, hv=1, dk=128, dv=128, out=F32),
     "f32_d128_ragged": dict(lengths=RAGGED, hk=2, hv=4, dk=128, dv=128, io=F32, out=F32),
@@ -293,6 +296,32 @@ def test_prefill_offsets_that_are_not_ascending(B, io):
         for b in range(3):
             if not 0 <= bad[b] <= bad[b + 1] <= c.n:
                 assert torch.equal(S[int(c.slots[b])], c.S[int(c.slots[b])])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("pairs", [3, 40, 90])
+def test_prefill_offsets_that_start_over(B, io, pairs):
+    """Offsets that go back are a fault from there on: the sequences before are computed, and the
+    workspace, which could not hold overlapping sequences, is not left."""
+    n = 64 * pairs + 508  # more than 32 a sequence: bf16 takes the chunks
+    c = Linear([n] + [0] * (2 * pairs - 2), 1, 2, 128, 128, io, F32)
+    c.offsets = torch.tensor(([0, n] * pairs)[:2 * pairs], dtype=torch.int32, device="cuda")
+    size = B.lq_linear_workspace_bytes(c.cfg(B), n)
+    ws = torch.full((size + (64 << 20),), 171, dtype=torch.uint8, device="cuda")
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o, ws=ws[:size] if size else None)
+    assert bool((ws[size:] == 171).all())
+    assert B.lq_get_error_word(c.err) == B.LQ_ERR_DEVICE_BOUNDS
+    c.err.zero_()
+    c.check(o, S, skip=range(1, c.b))
+    # offsets that leave the rows but ascend: only the sequences past the rows are left out
+    d = Linear([n, 0, 5], 1, 2, 128, 128, io, F32)
+    d.offsets = torch.tensor([0, n, n + 9, n + 9], dtype=torch.int32, device="cuda")
+    S, o = d.S.clone(), d.new_out()
+    d.prefill(B, S, o)
+    assert B.lq_get_error_word(d.err) == B.LQ_ERR_DEVICE_BOUNDS
+    d.err.zero_()
+    d.check(o, S, skip=(1, 2))
 
 
 def test_prefill_then_steps_is_one_prefill(B):
