@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(kNT) linear_tokens_kernel(const LinParams p, c
   const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
   if (!OUT && !sg.partial && !last) return;  // no outputs asked for: the last state alone
   const int64_t begin = pl.first + pl.index * sg.tokens;
-  const int count = min(sg.tokens, pl.length - pl.index * sg.tokens);
+  const int rest = pl.length - pl.index * sg.tokens;
+  const int count = pl.count > 1 ? min(sg.tokens, rest) : rest;
   if (count == 0 && !fresh) return;
 
   const int stages = (count + kTok - 1) / kTok;
@@ -293,7 +294,8 @@ size_t linear_tokens_workspace(const LinParams &p) {
 }
 
 cudaError_t launch_linear_tokens(const LinParams &p, void *workspace, cudaStream_t st) {
-  const Segments sg = segments_in(p, tokens_segment(p), workspace);
+  const int segment = tokens_segment(p);
+  const Segments sg = segments_in(p, segment, segment, workspace);
   if (p.dk == 32) return tokens_d<32>(p, sg, st);
   if (p.dk == 64) return tokens_d<64>(p, sg, st);
   return tokens_d<128>(p, sg, st);

@@ -91,6 +91,7 @@ __device__ __forceinline__ Span sequence_span(const LinParams &p, int b) {
 
 struct Segments {
   int tokens;      // tokens of a segment
+  int whole;       // a sequence of no more tokens than this is not cut
   bool partial;    // segments before a sequence's last: their own state, into the workspace
   float *states;   // workspace: per split sequence its first state, then each segment's state
   float *decays;   // workspace: [entry][Hv] the segments' whole decays
@@ -129,7 +130,7 @@ __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &s
     __syncthreads();
     const int length = b < p.B && b < found[5] ? sequence_span(p, b).count : -1;
     if (b < p.B) {
-      segs = length <= 0 ? 1 : (length + sg.tokens - 1) / sg.tokens;
+      segs = length <= sg.whole ? 1 : (length + sg.tokens - 1) / sg.tokens;
       cnt = sg.partial ? segs - 1 : segs;
       ent = segs > 1 ? segs : 0;
     }
@@ -202,7 +203,7 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
       if (descends != 0 && descent == kNoDescent) descent = j * 32 + __ffs(descends) - 1;
       const bool bad = j * 32 + lane >= descent || lo[j] < 0 || hi[j] > p.tokens;
       const int count = bad ? -1 : hi[j] - lo[j];
-      const int segs = j * 32 + lane >= p.B ? 0 : count <= 0 ? 1 : (count + sg.tokens - 1) / sg.tokens;
+      const int segs = j * 32 + lane >= p.B ? 0 : count <= sg.whole ? 1 : (count + sg.tokens - 1) / sg.tokens;
       const int cnt = sg.partial && segs > 0 ? segs - 1 : segs, ent = segs > 1 ? segs : 0;
       int c = cnt, e = ent;
 #pragma unroll
@@ -262,9 +263,9 @@ inline size_t segments_workspace(const LinParams &p, int segment) {
   const int64_t entries = 2 * split_segments(p, segment);
   return static_cast<size_t>(entries * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
 }
-inline Segments segments_in(const LinParams &p, int segment, void *workspace) {
+inline Segments segments_in(const LinParams &p, int segment, int whole, void *workspace) {
   float *states = static_cast<float *>(workspace);
-  return {segment, false, states,
+  return {segment, whole, false, states,
           states + 2 * split_segments(p, segment) * p.Hv * p.dk * p.dv};
 }
 

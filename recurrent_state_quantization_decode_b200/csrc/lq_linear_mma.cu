@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kC = 128;        // tokens of a chunk
 constexpr int kNT = 768;
-constexpr uint32_t kPolls = 1u << 18;  // of 64 polls each
+constexpr uint32_t kPolls = 1u << 11;  // of 64 polls of at most 20 us each: a wait ends within 3 s
 
 struct Decays {
   float a[kC];     // the tokens' decays, 1 behind the last token
@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(kNT, 1)
   const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
   if (STATES && !sg.partial && !last) return;  // no outputs asked for: the last state alone
   const int first = pl.first + pl.index * sg.tokens;
-  const int n = min(sg.tokens, pl.length - pl.index * sg.tokens);
+  const int rest = pl.length - pl.index * sg.tokens;
+  const int n = pl.count > 1 ? min(sg.tokens, rest) : rest;
   const int chunks = (n + kC - 1) / kC;
   if (chunks == 0 && !fresh) return;
   const int64_t tile = static_cast<int64_t>(p.dv) * p.dk;
@@ -965,11 +966,12 @@ cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4],
 // segments of every head take `waves` rounds of n heads / SMs blocks; a round
 // costs its chunks and about two more (its start and its end).  The segments'
 // own states, which a second launch needs first, cost about half of that again:
-// a call is split only where it gains more.  Sequences shorter than a segment
-// stay whole.
+// a call is split only where it gains more.  Several sequences keep the SMs
+// busy side by side: pieces of one need not be shorter than an SM's share of
+// the call.
 int linear_segment(const LinParams &p) {
   constexpr int kSMs = 148;
-  const int64_t chunks = (p.tokens + kC - 1) / kC;
+  const int64_t chunks = (static_cast<int64_t>(p.tokens) + kC - 1) / kC;
   int64_t best = chunks, cost = chunks + 2;
   for (int waves = 1; waves <= 4; ++waves) {
     const int64_t n = kSMs * waves / p.Hv;
@@ -978,7 +980,20 @@ int linear_segment(const LinParams &p) {
     const int64_t c = waves * (each + 2) * 3 / 2;
     if (c < cost) best = each, cost = c;
   }
-  return static_cast<int>(best < 1 ? 1 : best) * kC;
+  const int64_t share = (chunks * p.Hv + kSMs - 1) / kSMs;
+  if (p.B > 1 && best < share) best = share;
+  if (p.B > 1 && best + best / 2 >= chunks) best = chunks;  // no sequence to cut, see below
+  const int64_t tokens = (best < 1 ? 1 : best) * kC;
+  return static_cast<int>(tokens > 1 << 29 ? 1 << 29 : tokens);
+}
+
+// The longest sequence that stays whole.  The states' pass makes a cut sequence
+// cost half as much again, so among several, one of up to one and a half shares
+// of an SM takes no longer whole: 24 prompts of 20,011 tokens in all, 32 heads,
+// the longest 1.4 shares, 262 us whole and 336 us cut; 9 prompts of 7,000
+// tokens, fp32 outputs, the longest 1.95 shares, 284 us whole and 223 us cut.
+static int longest_whole(const LinParams &p, int segment) {
+  return p.B > 1 && segment < p.tokens ? segment + segment / 2 : segment;
 }
 
 size_t linear_chunks_workspace(const LinParams &p) {
@@ -998,7 +1013,8 @@ cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream
         !encode(&m[3], p.out, p.tokens, p.Hv, p.dv, static_cast<int64_t>(p.Hv) * p.dv))
       return cudaErrorInvalidValue;
   }
-  const Segments sg = segments_in(p, linear_segment(p), workspace);
+  const int segment = linear_segment(p);
+  const Segments sg = segments_in(p, segment, longest_whole(p, segment), workspace);
   if (p.dk <= 64) return p.dv <= 64 ? launch_d<64, 64>(p, sg, m, st) : launch_d<64, 128>(p, sg, m, st);
   return p.dv <= 64 ? launch_d<128, 64>(p, sg, m, st) : launch_d<128, 128>(p, sg, m, st);
 }
