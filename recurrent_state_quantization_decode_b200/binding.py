@@ -384,9 +384,10 @@ def _rows(x, stride: int, dev: int, what: str) -> Optional[int]:
         return x
     if x.get_device() != dev:
         raise ValueError(f"{what}: the tensor must be on the current CUDA device")
-    if stride and x.dim() == 3 and x.stride(2) == 1 and x.stride(1) == x.size(2) and \
-            x.stride(0) == stride:
-        return x.data_ptr()
+    if stride:
+        s = x.stride()
+        if len(s) == 3 and s[0] == stride and s[2] == 1 and s[1] == x.size(2):
+            return x.data_ptr()
     if stride or not x.is_contiguous():
         n, s, row = x.shape, x.stride(), 1
         for i in range(x.dim() - 1, 0, -1):

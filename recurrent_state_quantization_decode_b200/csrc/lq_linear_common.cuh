@@ -252,6 +252,31 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
   return !fault;
 }
 
+// The second launch of a call in segments may start while the first one's last
+// blocks run (its blocks then find their places, fetch their first tokens and
+// wait here before they touch a state).  No effect in a launch of its own.
+__device__ __forceinline__ void wait_for_states() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... Params, class... Args>
+cudaError_t launch_next(void (*kernel)(Params...), int64_t grid, int threads, int smem, bool overlaps,
+                        cudaStream_t st, const Args &...args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlaps ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // At most how many segments come before a sequence's last one.
 inline int64_t split_segments(const LinParams &p, int segment) {
   return p.tokens > segment ? p.tokens / segment : 0;

@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kNT, 1)
   float *entry = sg.states + (static_cast<int64_t>(pl.entry) * p.Hv + h) * tile;
   const int64_t entry_step = static_cast<int64_t>(p.Hv) * tile;
 
+  if (sg.partial) let_next_start();
   const uint32_t base = tc::smem_addr(smem);
   volatile int *dead = &ctl.dead;
   const uint32_t bars = base + T::kControl + static_cast<uint32_t>(offsetof(Control, bar));
@@ -672,6 +673,7 @@ __global__ void __launch_bounds__(kNT, 1)
           *reinterpret_cast<float4 *>(row + f) = make_float4(S[f], S[f + 1], S[f + 2], S[f + 3]);
       }
     };
+    wait_for_states();
     if (!fresh && sg.partial && pl.index == 0) {
       // a split sequence's first state moves to the workspace: the block of
       // the last segment writes the pool while others still need it
@@ -926,7 +928,7 @@ bool encode(CUtensorMap *map, const void *p, int tokens, int heads, int d, int64
 
 template <int DKP, int DVP, bool F32OUT, bool STATES>
 cudaError_t launch_t(const LinParams &p, const Segments &sg, const CUtensorMap (&m)[4], int64_t grid,
-                     cudaStream_t st) {
+                     bool overlaps, cudaStream_t st) {
   auto kernel = linear_chunks_kernel<DKP, DVP, F32OUT, STATES>;
   // once for each device
   static std::atomic<uint64_t> ready{0};
@@ -940,9 +942,8 @@ cudaError_t launch_t(const LinParams &p, const Segments &sg, const CUtensorMap (
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  kernel<<<static_cast<unsigned>(grid), kNT, Tiles<DKP, DVP>::kBytes, st>>>(p, sg, m[0], m[1], m[2],
-                                                                              m[3]);
-  return cudaGetLastError();
+  return launch_next(kernel, grid, kNT, Tiles<DKP, DVP>::kBytes, overlaps, st, p, sg, m[0], m[1], m[2],
+                     m[3]);
 }
 
 template <int DKP, int DVP>
@@ -950,14 +951,15 @@ cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4],
   const int64_t split = split_segments(p, sg.tokens);
   if (split > 0) {
     sg.partial = true;
-    const cudaError_t e = launch_t<DKP, DVP, false, true>(p, sg, m, split * p.Hv, st);
+    const cudaError_t e = launch_t<DKP, DVP, false, true>(p, sg, m, split * p.Hv, false, st);
     if (e != cudaSuccess) return e;
     sg.partial = false;
   }
   const int64_t grid = (split + p.B) * p.Hv;
-  if (p.out == nullptr) return launch_t<DKP, DVP, false, true>(p, sg, m, grid, st);
-  if (p.out_bf16) return launch_t<DKP, DVP, false, false>(p, sg, m, grid, st);
-  return launch_t<DKP, DVP, true, false>(p, sg, m, grid, st);
+  const bool over = split > 0;
+  if (p.out == nullptr) return launch_t<DKP, DVP, false, true>(p, sg, m, grid, over, st);
+  if (p.out_bf16) return launch_t<DKP, DVP, false, false>(p, sg, m, grid, over, st);
+  return launch_t<DKP, DVP, true, false>(p, sg, m, grid, over, st);
 }
 
 }  // namespace
