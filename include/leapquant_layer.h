@@ -96,7 +96,10 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  *    results (operands go in as exact sums of bf16 parts), bf16 outputs may
  *    see the state rounded once to bf16.  Decays enter as products over ranges
  *    of tokens, never as quotients: a decay of 0 (a reset) and long chains of
- *    small ones give exact zeros. */
+ *    small ones give exact zeros.  An infinite or NaN v shows in its
+ *    channel of its sequence's outputs from the start of its chunk on, where the
+ *    recurrence has it from its token on; nothing else sees it.
+ *  - out may not overlap the inputs. */
 size_t lq_linear_workspace_bytes(const lq_linear_config *cfg, int32_t tokens);
 lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const void *k,
                             const void *v, const float *decay, int32_t tokens,

@@ -324,6 +324,29 @@ def test_prefill_offsets_that_start_over(B, io, pairs):
     d.check(o, S, skip=(1, 2))
 
 
+@pytest.mark.parametrize("io,out", [(BF, BF), (BF, F32), (F32, F32)])
+def test_prefill_values_that_are_not_finite(B, io, out):
+    """They stay in their sequence, head and channel, and in bf16 prompts within their chunk before
+    their token (fp32 prompts: not before it at all)."""
+    c = Linear([300, 150], 1, 2, 128, 128, io, out, seed=8)
+    S0, o0 = c.S.clone(), c.new_out()
+    c.prefill(B, S0, o0)
+    for bad in (math.inf, math.nan):
+        v = c.v.clone()
+        c.v[200, 1, 37] = bad
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o)
+        c.v = v
+        assert not bool(o[200:300, 1, 37].isfinite().any())
+        assert not bool(S[int(c.slots[0]), 1, 37].isfinite().any())
+        o[200:300, 1, 37] = o0[200:300, 1, 37]
+        if io == BF:
+            o[128:200, 1, 37] = o0[128:200, 1, 37]
+        S[int(c.slots[0]), 1, 37] = S0[int(c.slots[0]), 1, 37]
+        assert torch.equal(o, o0) and torch.equal(S, S0)
+    assert int(c.err) == 0
+
+
 def test_prefill_then_steps_is_one_prefill(B):
     """A prompt in two calls and single tokens end where one call ends."""
     for io, out in ((BF, F32), (F32, F32)):
