@@ -102,7 +102,8 @@ struct TokensMap {
       const float4 v = load_four<BF16>(row, col(lane, 0));
       x[0] = make_float2(v.x, v.y), x[1] = make_float2(v.z, v.w);
     } else if constexpr (BF16) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + lane % LPR * 16);
+      const char *at = static_cast<const char *>(row) + lane % LPR * 16;
+      const uint4 v = *reinterpret_cast<const uint4 *>(at);
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -110,7 +111,7 @@ struct TokensMap {
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + col(lane, i));
+        const float4 v = load_four<false>(row, col(lane, i));
         x[2 * i] = make_float2(v.x, v.y), x[2 * i + 1] = make_float2(v.z, v.w);
       }
     }
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(kNT) linear_tokens_kernel(const LinParams p, c
   double total = 1.0;  // the segment's whole decay
   // the lane's output of a group: token mine / NP, row mine % NP of its rows
   const int mine = lane % M::LPR;
-  int64_t to = ((begin + mine / M::NP) * p.Hv + h) * p.dv + block0 + row0 + M::row(lane) + mine % M::NP;
+  int64_t to = ((begin + mine / M::NP) * p.Hv + h) * p.dv + block0 + row0 + M::row(lane) +
+               mine % M::NP;
   const int64_t to_step = static_cast<int64_t>(kGroup) * p.Hv * p.dv;
 #pragma unroll 1
   for (int st = 0; st < stages; ++st) {

@@ -203,7 +203,8 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
       if (descends != 0 && descent == kNoDescent) descent = j * 32 + __ffs(descends) - 1;
       const bool bad = j * 32 + lane >= descent || lo[j] < 0 || hi[j] > p.tokens;
       const int count = bad ? -1 : hi[j] - lo[j];
-      const int segs = j * 32 + lane >= p.B ? 0 : count <= sg.whole ? 1 : (count + sg.tokens - 1) / sg.tokens;
+      const int pieces = count <= sg.whole ? 1 : (count + sg.tokens - 1) / sg.tokens;
+      const int segs = j * 32 + lane >= p.B ? 0 : pieces;
       const int cnt = sg.partial && segs > 0 ? segs - 1 : segs, ent = segs > 1 ? segs : 0;
       int c = cnt, e = ent;
 #pragma unroll

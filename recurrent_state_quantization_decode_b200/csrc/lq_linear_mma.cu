@@ -57,10 +57,14 @@ struct Decays {
   float a[kC];     // the tokens' decays, 1 behind the last token
   float rest[kC];  // a_{j+1} ... to the end of j's block of 32 tokens
 };
-// The block's barriers; those up to kRingEmpty come in pairs, one a stage or slot.
+// The block's barriers; those up to kStaged come in pairs, one a stage or slot.
+// A single one's next phase needs what follows the wait for the last; outputs
+// can be staged before the warp that stores them has seen the chunk before.
 enum Barrier : uint32_t {
-  kFullQK = 0, kFullV = 2, kEmptyQ = 4, kEmptyK = 6, kEmptyV = 8, kDecFull = 10, kDecEmpty = 12, kRingFull = 14, kRingEmpty = 16,
-  kPFull = 18, kPDone, kSReady, kQSPart, kQSDone, kOScaled, kOFull, kOEmpty, kSFull, kGrownRead, kStaged, kStored, kTail,
+  kFullK = 0, kFullV = 2, kFullQ = 4, kEmptyQ = 6, kEmptyK = 8, kEmptyV = 10, kDecFull = 12,
+  kDecEmpty = 14, kRingFull = 16, kRingEmpty = 18, kStaged = 20,
+  kPFull = 22, kPDone, kSReady, kQSPart, kQSDone, kOScaled, kOFull, kOEmpty, kSFull, kGrownRead,
+  kStored, kTail,
   kBarriers
 };
 struct Control {
@@ -251,7 +255,9 @@ __global__ void __launch_bounds__(kNT, 1)
   __syncthreads();  // what locate left in shared memory is read
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      tc::bar_init(at(kFullQK + s), 1);
+      tc::bar_init(at(kFullK + s), 1);
+      tc::bar_init(at(kFullQ + s), 1);
+      tc::bar_init(at(kStaged + s), 8);
       tc::bar_init(at(kFullV + s), 1);
       tc::bar_init(at(kEmptyQ + s), T::kOverQ && !F32OUT ? 2 : 1);
       tc::bar_init(at(kEmptyK + s), STATES ? 1 : 2);
@@ -271,7 +277,6 @@ __global__ void __launch_bounds__(kNT, 1)
     tc::bar_init(at(kOEmpty), 8);
     tc::bar_init(at(kSFull), 1);
     tc::bar_init(at(kGrownRead), SWARPS);
-    tc::bar_init(at(kStaged), 8);
     tc::bar_init(at(kStored), 1);
     tc::bar_init(at(kTail), SWARPS);
     ctl.dead = (base & 1023) != 0;  // never: the tiles' alignment
@@ -295,104 +300,106 @@ __global__ void __launch_bounds__(kNT, 1)
   if (!sound) {
   } else if (warp >= 20) {
     set_registers_down<64>();
+    // The issuing warps run as a whole, which leaves their operands' addresses in
+    // uniform registers, and one lane issues (by a single thread's code 32,768
+    // tokens, 32 heads took 476 us where this takes 451).
+    const uint32_t lead = tc::elect();
     if (warp == 20) {
-      if (lane == 0) {
-        constexpr uint32_t kShapeQK = tc::product_shape(kC, kC, false, false);
-        constexpr uint32_t kShapeQS = tc::product_shape(kC, DVP, false, false);
-        constexpr uint32_t kShapePV = tc::product_shape(kC, DVP, false, true);
-        if constexpr (!STATES) {
-          auto scores = [&](int c) {
-            const uint32_t q = anew(tc::operand(base + (c & 1) * T::kStage, 0));
+      constexpr uint32_t kShapeQK = tc::product_shape(kC, kC, false, false);
+      constexpr uint32_t kShapeQS = tc::product_shape(kC, DVP, false, false);
+      constexpr uint32_t kShapePV = tc::product_shape(kC, DVP, false, true);
+      if constexpr (!STATES) {
+        auto scores = [&](int c) {
+          const uint32_t q = tc::operand(base + (c & 1) * T::kStage, 0);
 #pragma unroll
-            for (int i = 0; i < DKP / 16; ++i)
-              tc::product_ss(tm + kP, q + row_step(i, kC), q + T::kQ / 16 + row_step(i, kC),
-                             kShapeQK, i > 0);
-            tc::commit(at(kPFull));
-            tc::commit(at(kEmptyK + (c & 1)));
-          };
-          bool ok = chunks > 0 && wait_one(at(kFullQK), 0, dead, p.err);
-          if (ok) scores(0);
+          for (int i = 0; i < DKP / 16; ++i)
+            tc::product_ss(lead, tm + kP, q + row_step(i, kC), q + T::kQ / 16 + row_step(i, kC),
+                           kShapeQK, i > 0);
+          tc::commit(lead, at(kPFull));
+          tc::commit(lead, at(kEmptyK + (c & 1)));
+        };
+        bool ok = chunks > 0 && wait_warp(at(kFullK), 0, dead, p.err) &&
+                  wait_warp(at(kFullQ), 0, dead, p.err);
+        if (ok) scores(0);
 #pragma unroll 1
-          for (int c = 0; ok && c < chunks; ++c) {
-            const int s = c & 1;
-            const uint32_t stage = base + s * T::kStage;
-            // Q S^T, part by part as the state's copies come
-            ok = c == 0 || wait_one(at(kOEmpty), (c - 1) & 1, dead, p.err);
+        for (int c = 0; ok && c < chunks; ++c) {
+          const int s = c & 1;
+          const uint32_t stage = base + s * T::kStage;
+          // Q S^T, part by part as the state's copies come
+          ok = c == 0 || wait_warp(at(kOEmpty), (c - 1) & 1, dead, p.err);
 #pragma unroll 1
-            for (int part = 0; ok && part < SPARTS; ++part) {
-              ok = wait_one(at(kSReady), (c * SPARTS + part) & 1, dead, p.err);
-              if (!ok) break;
-              tc::after_sync();
-              const uint32_t q = anew(tc::operand(stage, 0));
-              const uint32_t state = anew(tc::operand(base + T::kState, 0));
-#pragma unroll
-              for (int i = 0; i < DKP / 16; ++i)
-                tc::product_ss(tm + kO, q + row_step(i, kC), state + row_step(i, DVP), kShapeQS,
-                               i > 0 || part > 0);
-              tc::commit(part < SPARTS - 1 ? at(kQSPart) : at(kQSDone));
-            }
-            if (!ok) break;
-            tc::commit(at(kEmptyQ + s));
-            // (W o P) V onto G (Q S^T), the small parts first
-            ok = wait_one(at(kFullV + s), (c >> 1) & 1, dead, p.err) &&
-                 (n - c * kC >= kC || wait_one(at(kTail), 0, dead, p.err)) &&
-                 wait_one(at(kPDone), c & 1, dead, p.err) &&
-                 wait_one(at(kOScaled), c & 1, dead, p.err);
+          for (int part = 0; ok && part < SPARTS; ++part) {
+            ok = wait_warp(at(kSReady), (c * SPARTS + part) & 1, dead, p.err);
             if (!ok) break;
             tc::after_sync();
-            const uint32_t v = anew(tc::operand(stage + 2 * T::kQ, kC * 128));
-#pragma unroll 1
-            for (int part = PARTS - 1; part >= 0; --part)
+            const uint32_t q = tc::operand(stage, 0);
+            const uint32_t state = tc::operand(base + T::kState, 0);
 #pragma unroll
-              for (int i = 0; i < kC / 16; ++i)
-                tc::product_ts(tm + kO, tm + weight_column(part, i), v + column_step(i), kShapePV,
-                               true);
-            tc::commit(at(kOFull));
-            tc::commit(at(kEmptyV + s));
-            // the next scores, over W o P, which is read by then
-            if (c + 1 < chunks) {
-              ok = wait_one(at(kFullQK + (s ^ 1)), ((c + 1) >> 1) & 1, dead, p.err) &&
-                   wait_one(at(kOFull), c & 1, dead, p.err);
-              if (ok) scores(c + 1);
-            }
+            for (int i = 0; i < DKP / 16; ++i)
+              tc::product_ss(lead, tm + kO, q + row_step(i, kC), state + row_step(i, DVP), kShapeQS,
+                             i > 0 || part > 0);
+            tc::commit(lead, part < SPARTS - 1 ? at(kQSPart) : at(kQSDone));
+          }
+          if (!ok) break;
+          tc::commit(lead, at(kEmptyQ + s));
+          // (W o P) V onto G (Q S^T), the small parts first
+          ok = wait_warp(at(kFullV + s), (c >> 1) & 1, dead, p.err) &&
+               (n - c * kC >= kC || wait_warp(at(kTail), 0, dead, p.err)) &&
+               wait_warp(at(kPDone), c & 1, dead, p.err) &&
+               wait_warp(at(kOScaled), c & 1, dead, p.err);
+          if (!ok) break;
+          tc::after_sync();
+          const uint32_t v = tc::operand(stage + 2 * T::kQ, kC * 128);
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+            for (int i = 0; i < kC / 16; ++i)
+              tc::product_ts(lead, tm + kO, tm + weight_column(part, i), v + column_step(i), kShapePV,
+                             true);
+          tc::commit(lead, at(kOFull));
+          tc::commit(lead, at(kEmptyV + s));
+          // the next scores, over W o P, which is read by then
+          if (c + 1 < chunks) {
+            ok = wait_warp(at(kFullK + (s ^ 1)), ((c + 1) >> 1) & 1, dead, p.err) &&
+                 wait_warp(at(kFullQ + (s ^ 1)), ((c + 1) >> 1) & 1, dead, p.err) &&
+                 wait_warp(at(kOFull), c & 1, dead, p.err);
+            if (ok) scores(c + 1);
           }
         }
       }
     } else if (warp == 22) {
-      if (lane == 0) {
-        // (w V)^T K, 32 tokens at a time, the small parts first.  The value
-        // channels are padded to 128 rows, of which those behind DVP are never
-        // read.
-        constexpr uint32_t kShapeS = tc::product_shape(128, DKP, false, true);
-        bool ok = true;
+      // (w V)^T K, 32 tokens at a time, the small parts first.  The value
+      // channels are padded to 128 rows, of which those behind DVP are never
+      // read.
+      constexpr uint32_t kShapeS = tc::product_shape(128, DKP, false, true);
+      bool ok = true;
 #pragma unroll 1
-        for (int c = 0; ok && c < chunks; ++c) {
-          const int s = c & 1;
-          // the state's warps have taken the last increment
-          ok = wait_one(at(kFullQK + s), (c >> 1) & 1, dead, p.err) &&
-               (n - c * kC >= kC || wait_one(at(kTail), 0, dead, p.err)) &&
-               (c == 0 || wait_one(at(kGrownRead), (c - 1) & 1, dead, p.err));
-          uint32_t k = tc::operand(base + s * T::kStage + T::kQ, kC * 128);
+      for (int c = 0; ok && c < chunks; ++c) {
+        const int s = c & 1;
+        // the state's warps have taken the last increment
+        ok = wait_warp(at(kFullK + s), (c >> 1) & 1, dead, p.err) &&
+             (n - c * kC >= kC || wait_warp(at(kTail), 0, dead, p.err)) &&
+             (c == 0 || wait_warp(at(kGrownRead), (c - 1) & 1, dead, p.err));
+        uint32_t k = tc::operand(base + s * T::kStage + T::kQ, kC * 128);
 #pragma unroll 1
-          for (int r = 0; ok && r < 4; ++r) {
-            const int fill = 4 * c + r, slot = fill % RING;
-            ok = wait_one(at(kRingFull + slot), (fill / RING) & 1, dead, p.err);
-            if (!ok) break;
-            tc::after_sync();
-            const uint32_t a = anew(tm + kRing + slot * kSlot);
-#pragma unroll
-            for (int part = 2; part >= 0; --part)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                tc::product_ts(tm + kGrown, a + part * 16 + i * 8, k + column_step(i), kShapeS,
-                               r > 0 || i > 0 || part < 2);
-            tc::commit(at(kRingEmpty + slot));
-            k = anew(k + 2 * column_step(1));
-          }
+        for (int r = 0; ok && r < 4; ++r) {
+          const int fill = 4 * c + r, slot = fill % RING;
+          ok = wait_warp(at(kRingFull + slot), (fill / RING) & 1, dead, p.err);
           if (!ok) break;
-          tc::commit(at(kSFull));
-          tc::commit(at(kEmptyK + s));
+          tc::after_sync();
+          const uint32_t a = tm + kRing + slot * kSlot;
+#pragma unroll
+          for (int part = 2; part >= 0; --part)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              tc::product_ts(lead, tm + kGrown, a + part * 16 + i * 8, k + column_step(i), kShapeS,
+                             r > 0 || i > 0 || part < 2);
+          tc::commit(lead, at(kRingEmpty + slot));
+          k = k + 2 * column_step(1);
         }
+        if (!ok) break;
+        tc::commit(lead, at(kSFull));
+        tc::commit(lead, at(kEmptyK + s));
       }
     } else if (warp == 21) {
       if (lane == 0) {
@@ -401,20 +408,25 @@ __global__ void __launch_bounds__(kNT, 1)
           const int s = c & 1, row = first + c * kC;
           const uint32_t before = ((c >> 1) - 1) & 1;
           const uint32_t q = base + s * T::kStage, k = q + T::kQ, v = k + T::kQ;
-          if (c >= 2 && !(wait_one(at(kEmptyK + s), before, dead, p.err) &&
-                          (STATES || wait_one(at(kEmptyQ + s), before, dead, p.err))))
-            break;
-          tc::bar_expect(at(kFullQK + s), STATES ? T::kQ : 2 * T::kQ);
+          // in the order in which the tiles before are done with, Q's last: its
+          // place holds the outputs
+          if (c >= 2 && !wait_one(at(kEmptyK + s), before, dead, p.err)) break;
+          tc::bar_expect(at(kFullK + s), T::kQ);
 #pragma unroll
-          for (int x = 0; x < DKP; x += 64) {
-            tc::load_tile(k + x * (2 * kC), &mk, at(kFullQK + s), x, hk, row);
-            if (!STATES) tc::load_tile(q + x * (2 * kC), &mq, at(kFullQK + s), x, hk, row);
-          }
+          for (int x = 0; x < DKP; x += 64)
+            tc::load_tile(k + x * (2 * kC), &mk, at(kFullK + s), x, hk, row);
           if (c >= 2 && !wait_one(at(kEmptyV + s), before, dead, p.err)) break;
           tc::bar_expect(at(kFullV + s), T::kV);
 #pragma unroll
           for (int x = 0; x < DVP; x += 64)
             tc::load_tile(v + x * (2 * kC), &mv, at(kFullV + s), x, h, row);
+          if constexpr (!STATES) {
+            if (c >= 2 && !wait_one(at(kEmptyQ + s), before, dead, p.err)) break;
+            tc::bar_expect(at(kFullQ + s), T::kQ);
+#pragma unroll
+            for (int x = 0; x < DKP; x += 64)
+              tc::load_tile(q + x * (2 * kC), &mq, at(kFullQ + s), x, hk, row);
+          }
         }
       }
     } else {
@@ -471,10 +483,12 @@ __global__ void __launch_bounds__(kNT, 1)
       if (ok && chunks > 1) ok = decays(1);
 #pragma unroll 1
       for (int c = 0; ok && c < chunks; ++c) {
+        // before the wait for the outputs: all other warps need the decays
+        if (c + 2 < chunks && !(ok = decays(c + 2))) break;
         if constexpr (!STATES && !F32OUT) {
           // the chunk's outputs, unless they have left from registers
           const int s = c & 1;
-          if (!(ok = wait_warp(at(kStaged), c & 1, dead, p.err))) break;
+          if (!(ok = wait_warp(at(kStaged + s), (c >> 1) & 1, dead, p.err))) break;
           if (lane == 0 && staged(c)) {
             const uint32_t from = base + (T::kOverQ ? s * T::kStage : T::kOut);
 #pragma unroll
@@ -485,7 +499,6 @@ __global__ void __launch_bounds__(kNT, 1)
           arrive_warp(at(kStored));
           if (T::kOverQ) arrive_warp(at(kEmptyQ + s));
         }
-        if (c + 2 < chunks) ok = decays(c + 2);
       }
       if (sg.partial && lane == 0)
         sg.decays[static_cast<int64_t>(pl.entry + 1 + pl.index) * p.Hv + h] =
@@ -800,7 +813,7 @@ __global__ void __launch_bounds__(kNT, 1)
       arrive_warp(at(kOEmpty));
       if constexpr (!F32OUT) {
         tc::fence_async();
-        arrive_warp(at(kStaged));
+        arrive_warp(at(kStaged + (c & 1)));
       }
       return true;
     };
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(kNT, 1)
       const int live = n - c * kC;  // tokens of the chunk
       if (holds && live < kC) {
         // rows of other sequences behind the last token: nothing may come of them
-        ok = wait_warp(at(kFullQK + s), (c >> 1) & 1, dead, p.err) &&
+        ok = wait_warp(at(kFullK + s), (c >> 1) & 1, dead, p.err) &&
              wait_warp(at(kFullV + s), (c >> 1) & 1, dead, p.err);
         if (!ok) break;
         const int bt = (half * (SWARPS / 2) + quad) * 32 + lane;

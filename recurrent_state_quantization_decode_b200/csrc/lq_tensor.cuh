@@ -179,31 +179,41 @@ __device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t block) {
 }
 constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// D (tensor memory) = [D +] A B for one step of 16 along the contraction.
-__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
-                                           bool add) {
+// D (tensor memory) = [D +] A B for one step of 16 along the contraction; issued by
+// the lane with `lead`.
+__device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                           uint32_t shape, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %6, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
-                                           bool add) {
+__device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                           uint32_t shape, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %6, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh), "r"(lead)
       : "memory");
 }
-// The barrier gets one arrival when all products issued so far are done.
-__device__ __forceinline__ void commit(uint32_t bar) {
+// One lane of a warp, as 1 there and 0 elsewhere.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+               : "=r"(r));
+  return r;
+}
+// The barrier gets one arrival when all products that the lane has issued so far
+// are done.
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
-
 }  // namespace tc
 }  // namespace lq
