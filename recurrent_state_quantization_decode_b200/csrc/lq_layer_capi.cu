@@ -36,7 +36,8 @@ lq_status check_linear(const lq_linear_config *c, lq::LinParams *p) {
   // blocks (32 state rows each) and tiles are counted in 32 bits
   if (static_cast<int64_t>(c->batch) * c->num_v_heads * (c->dv / 32) > INT32_MAX)
     return LQ_ERR_UNSUPPORTED;
-  if (c->batch >= (1 << 19) || c->num_k_heads > 2048) return LQ_ERR_UNSUPPORTED;
+  // each block reads the earlier sequences' slots and lengths: a square of the batch
+  if (c->batch > (1 << 16) || c->num_k_heads > 2048) return LQ_ERR_UNSUPPORTED;
   std::memset(p, 0, sizeof(*p));
   if (!resolve_stride(c->q_stride, static_cast<int64_t>(c->num_k_heads) * c->dk, &p->q_stride) ||
       !resolve_stride(c->k_stride, static_cast<int64_t>(c->num_k_heads) * c->dk, &p->k_stride) ||

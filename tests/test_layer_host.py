@@ -63,6 +63,18 @@ def test_linear_config_is_checked(B, field, value, status):
     assert B.lq_linear_workspace_bytes(cfg, 100) == 0
 
 
+def test_linear_batch_has_a_limit(B):
+    """The blocks' work on slots and lengths grows with the batch's square."""
+    cfg = B.make_linear_config(65536, 1, 1, 64, 64)
+    assert B.lq_linear_workspace_bytes(cfg, 1 << 24) > 0
+    cfg.batch = 65537
+    assert B.lq_linear_workspace_bytes(cfg, 1 << 24) == 0
+    for call in (_step, _prefill):
+        with pytest.raises(B.LQError) as ei:
+            call(B, cfg)
+        assert ei.value.status == B.LQ_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(decay=None), 1), (dict(S=None), 1),
     (dict(err=None), 1), (dict(n=-1), 1), (dict(n=1), 1), (dict(q=GOOD + 8), 3), (dict(k=GOOD + 2), 3),
