@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kNT) linear_tokens_kernel(const LinParams p, c
   const int row0 = warp * 8;
   const int h = tile % p.Hv, hk = h / (p.Hv / p.Hk);
   Work pl;
-  if (!locate<kNT>(p, sg, tile / p.Hv, !sg.partial && h == 0 && block0 == 0, sm.scratch, pl)) return;
+  if (!locate<kNT, false>(p, sg, tile / p.Hv, !sg.partial && h == 0 && block0 == 0, sm.scratch, pl)) return;
   const int slot = pl.slot;
   const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
   if (!OUT && !sg.partial && !last) return;  // no outputs asked for: the last state alone

@@ -95,6 +95,34 @@ struct Segments {
   bool partial;    // segments before a sequence's last: their own state, into the workspace
   float *states;   // workspace: per split sequence its first state, then each segment's state
   float *decays;   // workspace: [entry][Hv] the segments' whole decays
+
+  __device__ __forceinline__ int pieces(int length) const {
+    return length <= whole ? 1 : (length + tokens - 1) / tokens;
+  }
+};
+
+// Where sequences longer than a segment stay whole, blocks are numbered through
+// the long sequences first: one that starts late adds its whole time to the
+// call's.  Pass 0 takes those whole ones, 1 the cut ones and all of more than
+// half a segment, 2 the rest.  24 prompts of 20,011 tokens, 32 heads, the longest
+// 1.4 segments: in the call's order 244 us with it first and 392 us with it last,
+// in passes 239 to 258 us in seven orders.
+//
+// A sequence's blocks count in its pass's 10 bits of a sum.  There are fewer than
+// 1,024: with several sequences a segment is an SM's share of the call at least,
+// so 148 cover it, cut or longer than half of one there are not more than twice
+// that, and at most kRankedMost sequences are ranked.
+constexpr int kRankedMost = 768;
+struct Rank {
+  int shift;
+  __device__ __forceinline__ Rank(const Segments &sg, int length) {
+    shift = length <= sg.tokens / 2 ? 20 : length <= sg.tokens || length > sg.whole ? 10 : 0;
+  }
+  // the blocks up to the sequence's last among those of its pass, and all of earlier passes
+  __device__ __forceinline__ int upto(unsigned prefix, unsigned all) const {
+    const int before = (shift > 0 ? all & 1023 : 0) + (shift > 10 ? all >> 10 & 1023 : 0);
+    return before + static_cast<int>(prefix >> shift & 1023);
+  }
 };
 
 // Where a block works.
@@ -115,10 +143,12 @@ constexpr int kPlaceInts = 2 * (NT / 32) + 6;
 // Segments are numbered through the sequences.  Whole block of NT threads;
 // `scratch` is kPlaceInts<NT> ints of shared memory.  Returns false if there
 // are fewer than `wanted` + 1.
-template <int NT>
+template <int NT, bool RANKED>
 __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &sg, int wanted,
                                            int *scratch, Place &pl) {
+  static_assert(!RANKED || NT >= kRankedMost, "ranked sequences are looked at together");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool ranked = RANKED && sg.whole > sg.tokens;
   int done = 0, entries = 0;
   int *found = scratch + 2 * (NT / 32);
   if (threadIdx.x == 0) found[0] = -1, found[5] = kNoDescent;
@@ -130,11 +160,12 @@ __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &s
     __syncthreads();
     const int length = b < p.B && b < found[5] ? sequence_span(p, b).count : -1;
     if (b < p.B) {
-      segs = length <= sg.whole ? 1 : (length + sg.tokens - 1) / sg.tokens;
+      segs = sg.pieces(length);
       cnt = sg.partial ? segs - 1 : segs;
       ent = segs > 1 ? segs : 0;
     }
-    int c = cnt, e = ent;
+    const Rank rank(sg, length);
+    int c = ranked ? cnt << rank.shift : cnt, e = ent;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int c2 = __shfl_up_sync(kAllLanes, c, o), e2 = __shfl_up_sync(kAllLanes, e, o);
@@ -149,7 +180,7 @@ __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &s
       if (w < warp) before += scratch[w], ebefore += scratch[(NT / 32) + w];
       done += scratch[w], entries += scratch[(NT / 32) + w];
     }
-    const int first = before + c - cnt;
+    const int first = (ranked ? rank.upto(before + c, done) : before + c) - cnt;
     if (wanted >= first && wanted < first + cnt) {
       found[0] = b;
       found[1] = wanted - first;
@@ -157,7 +188,7 @@ __device__ __forceinline__ bool find_place(const LinParams &p, const Segments &s
       found[3] = ebefore + e - ent;
       found[4] = length;
     }
-    if (wanted < done) break;
+    if (ranked || wanted < done) break;
   }
   __syncthreads();
   pl = {found[0], found[1], found[2], found[3], found[4]};
@@ -177,7 +208,7 @@ struct Work {
 // sequence's, offsets that do not ascend).  With `reports`, a fault goes into
 // the error word.  Up to 128 sequences every warp reads them all at once and
 // keeps them in registers, one round trip to L2 in place of four.
-template <int NT>
+template <int NT, bool RANKED>
 __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, int wanted,
                                        bool reports, int *scratch, Work &w) {
   const int lane = threadIdx.x & 31;
@@ -194,39 +225,48 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
         if (p.fresh != nullptr) fresh[j] = p.fresh[b] != 0;
       }
     }
-    int done = 0, entries = 0, descent = kNoDescent;
+    int segs[4], c[4], e[4];  // segments; blocks through the sequence's last; entries before it
+    int all = 0, entries = 0, descent = kNoDescent;
+    const bool ranked = RANKED && sg.whole > sg.tokens;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      segs[j] = c[j] = e[j] = 0;
+      if (j * 32 >= p.B) continue;
+      const unsigned descends = __ballot_sync(kAllLanes, hi[j] < lo[j]);
+      if (descends != 0 && descent == kNoDescent) descent = j * 32 + __ffs(descends) - 1;
+      const bool bad = j * 32 + lane >= descent || lo[j] < 0 || hi[j] > p.tokens;
+      hi[j] = bad ? -1 : hi[j] - lo[j];  // the length from here on
+      if (j * 32 + lane < p.B) segs[j] = sg.pieces(hi[j]);
+      const int cnt = sg.partial && segs[j] > 0 ? segs[j] - 1 : segs[j];
+      const int ent = segs[j] > 1 ? segs[j] : 0;
+      c[j] = ranked ? cnt << Rank(sg, hi[j]).shift : cnt, e[j] = ent;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int c2 = __shfl_up_sync(kAllLanes, c[j], o), e2 = __shfl_up_sync(kAllLanes, e[j], o);
+        if (lane >= o) c[j] += c2, e[j] += e2;
+      }
+      const int more = __shfl_sync(kAllLanes, c[j], 31), more_e = __shfl_sync(kAllLanes, e[j], 31);
+      c[j] += all, e[j] += entries - ent;
+      all += more, entries += more_e;
+    }
     unsigned hit = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (hit != 0 || j * 32 >= p.B) continue;
-      const unsigned descends = __ballot_sync(kAllLanes, hi[j] < lo[j]);
-      if (descends != 0 && descent == kNoDescent) descent = j * 32 + __ffs(descends) - 1;
-      const bool bad = j * 32 + lane >= descent || lo[j] < 0 || hi[j] > p.tokens;
-      const int count = bad ? -1 : hi[j] - lo[j];
-      const int pieces = count <= sg.whole ? 1 : (count + sg.tokens - 1) / sg.tokens;
-      const int segs = j * 32 + lane >= p.B ? 0 : pieces;
-      const int cnt = sg.partial && segs > 0 ? segs - 1 : segs, ent = segs > 1 ? segs : 0;
-      int c = cnt, e = ent;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int c2 = __shfl_up_sync(kAllLanes, c, o), e2 = __shfl_up_sync(kAllLanes, e, o);
-        if (lane >= o) c += c2, e += e2;
-      }
-      const int first = done + c - cnt;
+      const int cnt = sg.partial && segs[j] > 0 ? segs[j] - 1 : segs[j];
+      const int first = (ranked ? Rank(sg, hi[j]).upto(c[j], all) : c[j]) - cnt;
       hit = __ballot_sync(kAllLanes, wanted >= first && wanted < first + cnt);
       if (hit != 0) {
         const int from = __ffs(hit) - 1;
         w.b = j * 32 + from;
         w.index = wanted - __shfl_sync(kAllLanes, first, from);
-        w.count = __shfl_sync(kAllLanes, segs, from);
-        w.entry = __shfl_sync(kAllLanes, entries + e - ent, from);
+        w.count = __shfl_sync(kAllLanes, segs[j], from);
+        w.entry = __shfl_sync(kAllLanes, e[j], from);
         w.slot = __shfl_sync(kAllLanes, slots[j], from);
         w.first = __shfl_sync(kAllLanes, lo[j], from);
-        w.length = __shfl_sync(kAllLanes, count, from);
+        w.length = __shfl_sync(kAllLanes, hi[j], from);
         w.fresh = __shfl_sync(kAllLanes, fresh[j], from) != 0;
       }
-      done += __shfl_sync(kAllLanes, c, 31);
-      entries += __shfl_sync(kAllLanes, e, 31);
     }
     if (hit == 0) return false;
 #pragma unroll
@@ -237,7 +277,7 @@ __device__ __forceinline__ bool locate(const LinParams &p, const Segments &sg, i
     fault = w.slot >= p.num_slots || taken || w.length < 0;
   } else {
     Place pl;
-    if (!find_place<NT>(p, sg, wanted, scratch, pl)) return false;
+    if (!find_place<NT, RANKED>(p, sg, wanted, scratch, pl)) return false;
     w.b = pl.b, w.index = pl.index, w.count = pl.count, w.entry = pl.entry;
     w.slot = p.slots != nullptr ? p.slots[w.b] : w.b;
     w.first = p.offsets[w.b], w.length = pl.length;

@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kNT, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
   Work pl;
-  if (!locate<kNT>(p, sg, blockIdx.x / p.Hv, !sg.partial && h == 0, reinterpret_cast<int *>(smem),
-                   pl))
+  if (!locate<kNT, true>(p, sg, blockIdx.x / p.Hv, !sg.partial && h == 0,
+                         reinterpret_cast<int *>(smem), pl))
     return;
   const int slot = pl.slot;
   const bool last = pl.index == pl.count - 1, fresh = pl.fresh;
@@ -1004,11 +1004,12 @@ int linear_segment(const LinParams &p) {
 
 // The longest sequence that stays whole.  The states' pass makes a cut sequence
 // cost half as much again, so among several, one of up to one and a half shares
-// of an SM takes no longer whole: 24 prompts of 20,011 tokens in all, 32 heads,
-// the longest 1.4 shares, 262 us whole and 336 us cut; 9 prompts of 7,000
-// tokens, fp32 outputs, the longest 1.95 shares, 284 us whole and 223 us cut.
+// of an SM takes no longer whole if its blocks start first (Rank): 24 prompts of
+// 20,011 tokens in all, 32 heads, the longest 1.4 shares, 262 us whole and 336 us
+// cut; 9 prompts of 7,000 tokens, fp32 outputs, the longest 1.95 shares, 284 us
+// whole and 223 us cut.
 static int longest_whole(const LinParams &p, int segment) {
-  return p.B > 1 && segment < p.tokens ? segment + segment / 2 : segment;
+  return p.B > 1 && p.B <= kRankedMost && segment < p.tokens ? segment + segment / 2 : segment;
 }
 
 size_t linear_chunks_workspace(const LinParams &p) {

@@ -706,3 +706,75 @@ def test_norm_of_the_int8_decode_steps_outputs(B):
     want = o / torch.sqrt((o * o).mean(-1, keepdim=True) + 1e-5) * wt.double() * gate.double() * torch.sigmoid(
         gate.double())
     assert bool(((y.double() - want).abs() <= want.abs() * (R + 300 * U) + 1e-30).all())
+
+
+# ---------------------------------------------------------------------------
+# Linear attention: orders of the sequences
+# ---------------------------------------------------------------------------
+
+UNEVEN = [6000, 0, 3950, 130, 168, 127, 369, 381, 520, 2244, 165, 257, 211, 109, 197, 730, 779, 331, 943, 30, 183,
+          744, 913, 530]  # the longest 1.4 shares of an SM at 32 heads: it stays whole
+
+
+def _best_us(call):
+    """The shortest of several runs of ten calls."""
+    best = math.inf
+    for _ in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 100)
+    return best
+
+
+@pytest.mark.parametrize("spare", [0, 120])
+def test_prefill_orders(B, spare):
+    """The order of the sequences changes no bit, and where the longest stands not the call's time: long
+    ones start first (started last, the longest would add its whole time to the call's, 1.6 times as long
+    in all)."""
+    a = Linear(UNEVEN + [0] * spare, 16, 32, 128, 128, spare=0, seed=4)
+    b = Linear([0] * spare + UNEVEN[1:] + UNEVEN[:1], 16, 32, 128, 128, spare=0, seed=4)
+    order = list(range(len(UNEVEN), a.b)) + list(range(1, len(UNEVEN))) + [0]
+    rows = torch.cat([torch.arange(a.off[i], a.off[i + 1], device="cuda") for i in order])
+    b.q, b.k, b.v, b.decay = a.q[rows], a.k[rows], a.v[rows], a.decay[rows]
+    b.S, b.slots = a.S, a.slots[torch.tensor(order, device="cuda")]
+    took, got = [], []
+    for c in (a, b):
+        S, o = c.S.clone(), c.new_out()
+        ws = c.prefill(B, S, o)
+        got.append((S, o))
+        S, o = c.S.clone(), c.new_out()
+        took.append(_best_us(lambda: c.prefill(B, S, o, ws=ws)))
+        assert int(c.err) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1][rows], got[1][1])
+    assert took[1] <= 1.25 * took[0], took
+
+
+def test_prefill_of_a_long_sequence_among_many(B):
+    """More sequences than are ranked by length: a long one is cut wherever it stands."""
+    lengths = [1] * 500 + [30000] + [1] * 400
+    c = Linear(lengths, 1, 2, 64, 64, out=F32, spare=0, seed=6)
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o)
+    one = Linear([30000], 1, 2, 64, 64, out=F32, spare=0)
+    rows = slice(500, 30500)
+    one.q, one.k, one.v, one.decay = c.q[rows], c.k[rows], c.v[rows], c.decay[rows]
+    one.S, at = c.S[c.slots[500].long()][None].clone(), int(c.slots[500])
+    S1, o1 = one.S.clone(), one.new_out()
+    one.prefill(B, S1, o1)
+    for got, want in ((o[rows], o1), (S[at], S1[0])):  # fp32 results, cut in other places
+        assert float((got - want).norm()) <= 2e-5 * float(want.norm())
+    # the others are single tokens
+    rest = torch.cat([torch.arange(500, device="cuda"), torch.arange(30500, c.n, device="cuda")])
+    ids = torch.cat([torch.arange(500, device="cuda"), torch.arange(501, c.b, device="cuda")])
+    step = B.make_linear_config(900, 1, 2, 64, 64, in_bf16=True)
+    S2, o2 = c.S.clone(), torch.empty((900, 2, 64), device="cuda")
+    B.lq_linear_decode_step(step, c.q[rest], c.k[rest], c.v[rest], c.decay[rest], S2, c.num_slots, o2, c.err,
+                            slots=c.slots[ids])
+    used = c.slots[ids].long()
+    assert float((o[rest] - o2).norm()) <= 2e-5 * float(o2.norm())
+    assert float((S[used] - S2[used]).norm()) <= 2e-5 * float(S2[used].norm())
+    assert int(c.err) == 0 and int(one.err) == 0
