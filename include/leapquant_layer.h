@@ -91,8 +91,11 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  * fresh.  Arguments as for lq_linear_decode_step; decay per token is
  * [tokens][Hv].
  *  workspace: lq_linear_workspace_bytes(cfg, tokens) bytes, 16-byte aligned
- *  (nullable when that is 0).  Its contents matter during the call only; calls
- *  that may run at the same time, captured ones too, need one each.
+ *  (nullable when that is 0).  That is enough for every call of no more tokens
+ *  and no more sequences with cfg otherwise the same, so that a program can size
+ *  one buffer for its largest call (78 MB at most up to 2^29 tokens, d = 128).
+ *  Its contents matter during the call only; calls that may run at the same time,
+ *  captured ones too, need one each.
  *  - bf16 prompts are taken in chunks of 128 tokens whose products run on the
  *    tensor cores with fp32 accumulation; states and fp32 outputs are fp32
  *    results (operands go in as exact sums of bf16 parts), bf16 outputs may

@@ -46,8 +46,12 @@ struct NormParams {
 cudaError_t launch_linear_step(const LinParams &p, cudaStream_t stream);
 cudaError_t launch_linear_tokens(const LinParams &p, void *workspace, cudaStream_t stream);
 cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream_t stream);
+// What a prompt call needs, and the most that one of no more tokens and no more
+// sequences does.
 size_t linear_tokens_workspace(const LinParams &p);
 size_t linear_chunks_workspace(const LinParams &p);
+size_t linear_tokens_workspace_most(const LinParams &p);
+size_t linear_chunks_workspace_most(const LinParams &p);
 cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream);
 cudaError_t launch_group_norm(const NormParams &p, cudaStream_t stream);
 

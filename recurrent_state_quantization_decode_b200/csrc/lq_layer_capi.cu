@@ -109,8 +109,12 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
 size_t lq_linear_workspace_bytes(const lq_linear_config *cfg, int32_t tokens) {
   lq::LinParams p;
   if (check_linear(cfg, &p) != LQ_OK || tokens < 0) return 0;
+  // the most of both kernels over the calls that each may get
   p.tokens = tokens;
-  return by_chunks(p) ? lq::linear_chunks_workspace(p) : lq::linear_tokens_workspace(p);
+  const size_t chunks = p.in_bf16 ? lq::linear_chunks_workspace_most(p) : 0;
+  if (p.in_bf16 && tokens > 32 * static_cast<int64_t>(p.B)) p.tokens = 32 * p.B;
+  const size_t others = lq::linear_tokens_workspace_most(p);
+  return chunks > others ? chunks : others;
 }
 
 lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const void *k,
@@ -127,10 +131,11 @@ lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const vo
     return s;
   if (!aligned(offsets, 4) || !aligned(fresh, 4) || !aligned(workspace, 16))
     return LQ_ERR_MISALIGNED;
-  const size_t need = lq_linear_workspace_bytes(cfg, tokens);
+  p.tokens = tokens;
+  const size_t need =
+      by_chunks(p) ? lq::linear_chunks_workspace(p) : lq::linear_tokens_workspace(p);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return LQ_ERR_INVALID_ARG;
   if (cfg->batch == 0) return LQ_OK;
-  p.tokens = tokens;
   p.offsets = offsets;
   p.fresh = fresh;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -317,10 +317,12 @@ cudaError_t step_d(const LinParams &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+constexpr int64_t kBlocks = 148 * 5;
+
 // Tokens of a segment: so many that the segments' blocks fill the GPU about
 // once (5 of them an SM), but a launch's worth at least.
 int tokens_segment(const LinParams &p) {
-  constexpr int64_t kBlocks = 148 * 5, kLeast = 64;
+  constexpr int64_t kLeast = 64;
   const int64_t each = static_cast<int64_t>(p.tokens) * p.Hv * (p.dv / kRows) / kBlocks;
   const int64_t n = (each + kTok - 1) / kTok * kTok;
   return static_cast<int>(n < kLeast ? kLeast : n);
@@ -357,7 +359,16 @@ cudaError_t launch_linear_step(const LinParams &p, cudaStream_t st) {
 }
 
 size_t linear_tokens_workspace(const LinParams &p) {
-  return segments_workspace(p, tokens_segment(p));
+  return segments_workspace(p, split_segments(p, tokens_segment(p)));
+}
+
+// tokens_segment is 64 at least and more than x - 1 for x = tokens * blocks a
+// token / kBlocks, so that a call of x >= 64 has fewer than kBlocks / blocks *
+// 64 / 63 segments and any has at most tokens / 64.
+size_t linear_tokens_workspace_most(const LinParams &p) {
+  const int64_t some = p.tokens / 64;
+  const int64_t most = kBlocks * 64 / (63 * static_cast<int64_t>(p.Hv) * (p.dv / kRows));
+  return segments_workspace(p, some < most ? some : most);
 }
 
 cudaError_t launch_linear_tokens(const LinParams &p, void *workspace, cudaStream_t st) {

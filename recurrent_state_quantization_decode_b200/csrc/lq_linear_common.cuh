@@ -324,11 +324,10 @@ inline int64_t split_segments(const LinParams &p, int segment) {
   return p.tokens > segment ? p.tokens / segment : 0;
 }
 
-// Workspace of a call in segments: a sequence of s > 1 of them needs s entries,
-// a state and a decay each for every value head.
-inline size_t segments_workspace(const LinParams &p, int segment) {
-  const int64_t entries = 2 * split_segments(p, segment);
-  return static_cast<size_t>(entries * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
+// Workspace of a call with so many segments before a last one: a sequence of
+// s > 1 of them needs s entries, a state and a decay each for every value head.
+inline size_t segments_workspace(const LinParams &p, int64_t split) {
+  return static_cast<size_t>(2 * split * p.Hv * (static_cast<int64_t>(p.dk) * p.dv + 1) * 4);
 }
 inline Segments segments_in(const LinParams &p, int segment, int whole, void *workspace) {
   float *states = static_cast<float *>(workspace);

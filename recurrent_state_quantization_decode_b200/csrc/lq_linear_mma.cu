@@ -977,6 +977,8 @@ cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4],
 
 }  // namespace
 
+constexpr int kSMs = 148, kMostWaves = 4;
+
 // Tokens of a segment.  One block an SM walks over a segment, so that n
 // segments of every head take `waves` rounds of n heads / SMs blocks; a round
 // costs its chunks and about two more (its start and its end).  The segments'
@@ -985,10 +987,9 @@ cudaError_t launch_d(const LinParams &p, Segments sg, const CUtensorMap (&m)[4],
 // busy side by side: pieces of one need not be shorter than an SM's share of
 // the call.
 int linear_segment(const LinParams &p) {
-  constexpr int kSMs = 148;
   const int64_t chunks = (static_cast<int64_t>(p.tokens) + kC - 1) / kC;
   int64_t best = chunks, cost = chunks + 2;
-  for (int waves = 1; waves <= 4; ++waves) {
+  for (int waves = 1; waves <= kMostWaves; ++waves) {
     const int64_t n = kSMs * waves / p.Hv;
     if (n < 2) continue;
     const int64_t each = (chunks + n - 1) / n;
@@ -1013,7 +1014,16 @@ static int longest_whole(const LinParams &p, int segment) {
 }
 
 size_t linear_chunks_workspace(const LinParams &p) {
-  return segments_workspace(p, linear_segment(p));
+  return segments_workspace(p, split_segments(p, linear_segment(p)));
+}
+
+// linear_segment covers a call's chunks at most kSMs * 4 / heads times (any
+// number of sequences; a segment is one chunk at least), or by its limit of 2^29
+// tokens.
+size_t linear_chunks_workspace_most(const LinParams &p) {
+  const int64_t some = p.tokens / kC, cut = kSMs * kMostWaves / p.Hv, limit = p.tokens >> 29;
+  const int64_t most = cut > limit ? cut : limit;
+  return segments_workspace(p, some < most ? some : most);
 }
 
 cudaError_t launch_linear_chunks(const LinParams &p, void *workspace, cudaStream_t st) {

@@ -778,3 +778,17 @@ def test_prefill_of_a_long_sequence_among_many(B):
     assert float((o[rest] - o2).norm()) <= 2e-5 * float(o2.norm())
     assert float((S[used] - S2[used]).norm()) <= 2e-5 * float(S2[used].norm())
     assert int(c.err) == 0 and int(one.err) == 0
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_prefill_in_the_largest_calls_workspace(B, io):
+    """One workspace, sized for the largest call, serves all smaller ones, and nothing behind it is written."""
+    big = B.make_linear_config(6, 2, 8, 128, 128, in_bf16=io == BF)
+    size = B.lq_linear_workspace_bytes(big, 4000)
+    for lengths in ([129], [700], [1280], [1281], [2000, 1, 1999], [900, 0, 33, 1200, 7, 640], [4000]):
+        c = Linear(lengths, 2, 8, 128, 128, io, F32, seed=len(lengths))
+        ws = torch.full((size + (1 << 20),), 171, dtype=torch.uint8, device="cuda")
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o, ws=ws[:size])
+        c.check(o, S)
+        assert bool((ws[size:] == 171).all())

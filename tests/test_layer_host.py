@@ -200,3 +200,36 @@ def test_rotary_table_arguments_are_checked(B):
                  (64, 1e4, 3, 2.0, 0.0), (64, 1e4, 3, 2.0, 100.0, 1.0, 2.0)):
         assert _status(B, B.lq_rotary_table, *args) == B.LQ_ERR_INVALID_ARG, args
     assert _status(B, B.lq_rotary_table, 2048) == B.LQ_ERR_UNSUPPORTED
+
+
+def _accepts(B, cfg, tokens, space):
+    """Whether a prompt call takes a workspace of `space` bytes.  Without sequences it ends behind that
+    check: nothing is launched."""
+    empty = type(cfg).from_buffer_copy(cfg)
+    empty.batch = 0
+    status = B._lib.lq_linear_prefill(empty, GOOD, GOOD, GOOD, GOOD, tokens, GOOD, GOOD, 0, None, None, GOOD, GOOD,
+                                      space, GOOD, None)
+    assert status in (B.LQ_OK, B.LQ_ERR_INVALID_ARG)
+    return status == B.LQ_OK
+
+
+@pytest.mark.parametrize("hv,d,bf16", [(1, 128, True), (8, 128, True), (32, 128, True), (200, 32, True),
+                                       (600, 64, True), (1, 64, False), (8, 64, False), (32, 128, False),
+                                       (300, 32, False)])
+def test_workspace_of_the_largest_call_is_enough(B, hv, d, bf16):
+    """No smaller call, in tokens or in sequences, asks for more or is refused with the largest one's."""
+    def size(batch, tokens):
+        return B.lq_linear_workspace_bytes(B.make_linear_config(batch, hv, hv, d, d, in_bf16=bf16), tokens)
+
+    counts = sorted({0, 1, 32, 33, 63, 64, 127, 128, 129, 130, 10368, 10369} | {17 * i for i in range(1, 900)}
+                    | {128 * i + j for i in (5, 9, 81, 256, 1000, 5000) for j in (-1, 0, 1)}
+                    | {1 << 20, (1 << 29) - 1, 1 << 29, 1 << 30, (1 << 31) - 1})
+    for batch in (1, 2, 4, 24, 144, 1000):
+        sizes = [size(batch, n) for n in counts]
+        assert sizes == sorted(sizes), (batch, [n for n, a, b in zip(counts[1:], sizes, sizes[1:]) if b < a][:5])
+    for n in counts:
+        sizes = [size(b, n) for b in (1, 2, 3, 24, 144, 1000, 65536)]
+        assert sizes == sorted(sizes), n
+    cfg = B.make_linear_config(1, hv, hv, d, d, in_bf16=bf16)
+    for n in counts:
+        assert _accepts(B, cfg, n, size(1, n)), n
