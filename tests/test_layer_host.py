@@ -233,3 +233,16 @@ def test_workspace_of_the_largest_call_is_enough(B, hv, d, bf16):
     cfg = B.make_linear_config(1, hv, hv, d, d, in_bf16=bf16)
     for n in counts:
         assert _accepts(B, cfg, n, size(1, n)), n
+
+
+def test_workspace_below_the_need_is_refused(B):
+    """One byte less than what a call needs, found by halving, is an argument error."""
+    cfg = B.make_linear_config(1, 8, 8, 128, 128, in_bf16=True)
+    for n in (8192, 20000, 1 << 20):
+        least, most = 0, B.lq_linear_workspace_bytes(cfg, n)
+        assert most > 0 and _accepts(B, cfg, n, most) and not _accepts(B, cfg, n, 0)
+        while most - least > 1:
+            half = (least + most) // 2
+            least, most = (least, half) if _accepts(B, cfg, n, half) else (half, most)
+        assert most % (8 * (128 * 128 + 1) * 4) == 0  # whole states and decays of 8 heads
+        assert not _accepts(B, cfg, n, most - 1)
