@@ -349,15 +349,18 @@ def lq_get_last_error(state: lq_state, stream=None) -> int:
 # The layer operators (include/leapquant_layer.h), same names
 # ---------------------------------------------------------------------------
 
-_torch = None
+_torch = _F32 = _I32 = None
+_IO = {}  # lq_dtype -> torch's
 
 
 def _current():
     """(current device, current stream's handle) as torch has them; (-2, None)
     before torch has a CUDA context."""
-    global _torch
+    global _torch, _F32, _I32
     if _torch is None:
         import torch
+        _F32, _I32 = torch.float32, torch.int32
+        _IO.update({LQ_DTYPE_F32: torch.float32, LQ_DTYPE_BF16: torch.bfloat16})
         _torch = torch
     if not _torch.cuda.is_initialized():
         return -2, None
@@ -365,38 +368,53 @@ def _current():
     return dev, _torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _here(x, dev: int, what: str) -> Optional[int]:
-    """Address of a contiguous tensor on the current device (or an int, None)."""
+def _here(x, dev: int, what: str, dtype, least: int) -> Optional[int]:
+    """Address of a contiguous tensor of `dtype` (None: any) on the current
+    device that holds `least` values (or an int, which is taken as it is; None)."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != dev:
         raise ValueError(f"{what}: the tensor must be on the current CUDA device")
+    if x.dtype is not dtype and dtype is not None:
+        raise ValueError(f"{what}: the tensor must be {dtype}, not {x.dtype}")
     if not x.is_contiguous():
         raise ValueError(f"{what}: the tensor must be contiguous")
+    if x.numel() < least:
+        raise ValueError(f"{what}: the tensor holds {x.numel()} values, the call takes {least}")
     return x.data_ptr()
 
 
-def _rows(x, stride: int, dev: int, what: str) -> Optional[int]:
-    """Address of a token-major tensor [tokens, heads, d] on the current device
-    whose tokens lie `stride` elements apart (0: packed), each token's row
-    contiguous: a packed tensor or a slice of a fused projection's rows."""
+def _rows(x, stride: int, dev: int, what: str, dtype, tokens: int, row: int) -> Optional[int]:
+    """Address of a token-major tensor [tokens, heads, d] of `dtype` on the
+    current device whose tokens lie `stride` elements apart (0: packed), each
+    token's row of `row` values contiguous: a packed tensor or a slice of a fused
+    projection's rows.  An int is taken as it is; `row` 0 means that the call
+    does not look at it."""
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != dev:
         raise ValueError(f"{what}: the tensor must be on the current CUDA device")
+    if x.dtype is not dtype and dtype is not None and row:
+        raise ValueError(f"{what}: the tensor must be {dtype}, not {x.dtype}")
     if stride:
-        s = x.stride()
-        if len(s) == 3 and s[0] == stride and s[2] == 1 and s[1] == x.size(2):
+        n, s = x.shape, x.stride()
+        if len(s) == 3 and s[0] == stride and s[2] == 1 and s[1] == n[2] and n[0] >= tokens and \
+                n[1] * s[1] >= row:
             return x.data_ptr()
-    if stride or not x.is_contiguous():
-        n, s, row = x.shape, x.stride(), 1
-        for i in range(x.dim() - 1, 0, -1):
-            if n[i] != 1 and s[i] != row:
-                raise ValueError(f"{what}: a token's row must be contiguous")
-            row *= n[i]
-        if n[0] > 1 and row > 0 and s[0] != (stride or row):
-            raise ValueError(f"{what}: tokens lie {s[0]} elements apart, "
-                             f"the configuration says {stride or row}")
+    elif x.is_contiguous() and x.numel() >= tokens * row:
+        return x.data_ptr()
+    n, s, one = x.shape, x.stride(), 1
+    for i in range(x.dim() - 1, 0, -1):
+        if n[i] != 1 and s[i] != one:
+            raise ValueError(f"{what}: a token's row must be contiguous")
+        one *= n[i]
+    if x.dim() and n[0] > 1 and one > 0 and s[0] != (stride or one):
+        raise ValueError(f"{what}: tokens lie {s[0]} elements apart, "
+                         f"the configuration says {stride or one}")
+    held = 1 + sum((a - 1) * b for a, b in zip(n, s)) if x.numel() else 0
+    need = (tokens - 1) * (stride or row) + row if tokens > 0 and row > 0 else 0
+    if held < need:
+        raise ValueError(f"{what}: the tensor reaches over {held} values, the call over {need}")
     return x.data_ptr()
 
 
@@ -422,10 +440,16 @@ def lq_linear_decode_step(cfg, q, k, v, decay, S, num_slots: int, out, err, slot
     """One token of S <- a S + v k^T, o = S q for every sequence, states in
     the pool S [num_slots, Hv, dv, dk] updated in place."""
     dev, now = _current()
+    n, dk, hv, vrow = cfg.batch, cfg.dk, cfg.num_v_heads, cfg.num_v_heads * cfg.dv
+    io, krow = _IO.get(cfg.in_dtype), cfg.num_k_heads * dk
     _check(_lib.lq_linear_decode_step(
-        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q"), _rows(k, cfg.k_stride, dev, "k"),
-        _rows(v, cfg.v_stride, dev, "v"), _here(decay, dev, "decay"), _here(S, dev, "S"),
-        num_slots, _here(slots, dev, "slots"), _here(out, dev, "out"), _here(err, dev, "err"),
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q", io, n, krow),
+        _rows(k, cfg.k_stride, dev, "k", io, n, krow),
+        _rows(v, cfg.v_stride, dev, "v", io, n, vrow),
+        _here(decay, dev, "decay", _F32, hv if cfg.decay else n * hv),
+        _here(S, dev, "S", _F32, num_slots * vrow * dk), num_slots,
+        _here(slots, dev, "slots", _I32, n),
+        _here(out, dev, "out", _IO.get(cfg.out_dtype), n * vrow), _here(err, dev, "err", _I32, 1),
         _on(stream, now)), "lq_linear_decode_step")
 
 
@@ -444,13 +468,19 @@ def lq_linear_prefill(cfg, q, k, v, decay, tokens: int, offsets, S, num_slots: i
         space = lq_linear_workspace_bytes(cfg, tokens)
     else:
         space = workspace.nbytes
+    n, dk, hv, vrow = cfg.batch, cfg.dk, cfg.num_v_heads, cfg.num_v_heads * cfg.dv
+    io, krow = _IO.get(cfg.in_dtype), cfg.num_k_heads * dk
     _check(_lib.lq_linear_prefill(
-        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q"), _rows(k, cfg.k_stride, dev, "k"),
-        _rows(v, cfg.v_stride, dev, "v"), _here(decay, dev, "decay"), tokens,
-        _here(offsets, dev, "offsets"), _here(S, dev, "S"), num_slots,
-        _here(slots, dev, "slots"), _here(fresh, dev, "fresh"), _here(out, dev, "out"),
-        _here(workspace, dev, "workspace"), space, _here(err, dev, "err"), _on(stream, now)),
-        "lq_linear_prefill")
+        ctypes.byref(cfg), _rows(q, cfg.q_stride, dev, "q", io, tokens, krow),
+        _rows(k, cfg.k_stride, dev, "k", io, tokens, krow),
+        _rows(v, cfg.v_stride, dev, "v", io, tokens, vrow),
+        _here(decay, dev, "decay", _F32, hv if cfg.decay else tokens * hv), tokens,
+        _here(offsets, dev, "offsets", _I32, n + 1),
+        _here(S, dev, "S", _F32, num_slots * vrow * dk), num_slots,
+        _here(slots, dev, "slots", _I32, n), _here(fresh, dev, "fresh", _I32, n),
+        _here(out, dev, "out", _IO.get(cfg.out_dtype), tokens * vrow),
+        _here(workspace, dev, "workspace", None, 0), space, _here(err, dev, "err", _I32, 1),
+        _on(stream, now)), "lq_linear_prefill")
 
 
 def lq_rotary_table(rot: int, theta: float = 10000.0, scaling: int = LQ_ROPE_NONE,
@@ -480,11 +510,18 @@ def lq_rotary(cfg, tokens: int, q, k, positions, table, q_out, k_out, stream=Non
     """Rotates q and k (None without k heads) into q_out and k_out, which may
     be q and k themselves."""
     dev, now = _current()
+    io, d = _IO.get(cfg.dtype), cfg.d
+    qrow, krow = cfg.num_q_heads * d, cfg.num_k_heads * d
+    if hasattr(table, "element_size") and table.element_size() != 8:
+        raise ValueError(f"table: the tensor must hold 64-bit entries, not {table.dtype}")
     _check(_lib.lq_rotary(
-        ctypes.byref(cfg), tokens, _rows(q, cfg.q_stride, dev, "q"),
-        _rows(k, cfg.k_stride, dev, "k"), _here(positions, dev, "positions"),
-        _here(table, dev, "table"), _rows(q_out, cfg.q_out_stride, dev, "q_out"),
-        _rows(k_out, cfg.k_out_stride, dev, "k_out"), _on(stream, now)), "lq_rotary")
+        ctypes.byref(cfg), tokens, _rows(q, cfg.q_stride, dev, "q", io, tokens, qrow),
+        _rows(k, cfg.k_stride, dev, "k", io, tokens, krow),
+        _here(positions, dev, "positions", _I32, tokens),
+        _here(table, dev, "table", None, cfg.rot // 2),
+        _rows(q_out, cfg.q_out_stride, dev, "q_out", io, tokens, qrow),
+        _rows(k_out, cfg.k_out_stride, dev, "k_out", io, tokens, krow), _on(stream, now)),
+        "lq_rotary")
 
 
 def make_norm_config(groups: int, size: int, kind: int = LQ_NORM_RMS, act: int = LQ_ACT_SILU,
@@ -502,17 +539,21 @@ def lq_group_norm(cfg, tokens: int, x, out, gate=None, weight=None, bias=None,
                   stream=None) -> None:
     """Normalises each token's groups; act on the result, or on the gate."""
     dev, now = _current()
+    io, size = _IO.get(cfg.in_dtype), cfg.size
+    row = cfg.groups * size
     _check(_lib.lq_group_norm(
-        ctypes.byref(cfg), tokens, _rows(x, cfg.x_stride, dev, "x"),
-        _rows(gate, cfg.gate_stride, dev, "gate"), _here(weight, dev, "weight"),
-        _here(bias, dev, "bias"), _rows(out, cfg.out_stride, dev, "out"), _on(stream, now)),
-        "lq_group_norm")
+        ctypes.byref(cfg), tokens, _rows(x, cfg.x_stride, dev, "x", io, tokens, row),
+        _rows(gate, cfg.gate_stride, dev, "gate", io, tokens, row),
+        _here(weight, dev, "weight", _F32, size if cfg.shared_weight else row),
+        _here(bias, dev, "bias", _F32, row),
+        _rows(out, cfg.out_stride, dev, "out", _IO.get(cfg.out_dtype), tokens, row),
+        _on(stream, now)), "lq_group_norm")
 
 
 def lq_get_error_word(err, stream=None) -> int:
     """Synchronizes the stream, reads and clears the error word."""
     dev, now = _current()
-    return _lib.lq_get_error_word(_here(err, dev, "err"), _on(stream, now))
+    return _lib.lq_get_error_word(_here(err, dev, "err", _I32, 1), _on(stream, now))
 
 
 # ---------------------------------------------------------------------------

@@ -246,3 +246,118 @@ def test_workspace_below_the_need_is_refused(B):
             least, most = (least, half) if _accepts(B, cfg, n, half) else (half, most)
         assert most % (8 * (128 * 128 + 1) * 4) == 0  # whole states and decays of 8 heads
         assert not _accepts(B, cfg, n, most - 1)
+
+
+class _Fake:
+    """A library that launches nothing and takes every call."""
+
+    def __getattr__(self, name):
+        return lambda *args: 0
+
+
+@pytest.fixture
+def on_host(B, monkeypatch):
+    """The binding with host tensors taken for the current device's, and no library behind it."""
+    B._current()
+    monkeypatch.setattr(B, "_lib", _Fake())
+    monkeypatch.setattr(B, "_current", lambda: (-1, None))
+    return B
+
+
+def _bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _refused(call, good, bad):
+    """Takes the good arguments and refuses each changed one by its name."""
+    call(**good)
+    for name, x in bad:
+        with pytest.raises(ValueError, match=rf"^{name}: "):
+            call(**{**good, name: x})
+    call(**good)
+
+
+@pytest.mark.parametrize("head", [False, True])
+def test_linear_tensors_of_another_type_or_too_small_are_refused(on_host, head):
+    B, T, n, hk, hv, dk, dv = on_host, 9, 3, 2, 4, 32, 64
+    cfg = B.make_linear_config(n, hk, hv, dk, dv, in_bf16=True,
+                               decay=B.LQ_DECAY_HEAD if head else B.LQ_DECAY_TOKEN)
+    rows = _bf(T, 2 * hk * dk + hv * dv)
+    fused = B.make_linear_config(n, hk, hv, dk, dv, in_bf16=True, q_stride=rows.stride(0),
+                                 k_stride=rows.stride(0), v_stride=rows.stride(0),
+                                 decay=B.LQ_DECAY_HEAD if head else B.LQ_DECAY_TOKEN)
+
+    def cut(r):
+        a = hk * dk
+        return dict(q=r[:, :a].unflatten(1, (hk, dk)), k=r[:, a:2 * a].unflatten(1, (hk, dk)),
+                    v=r[:, 2 * a:].unflatten(1, (hv, dv)))
+
+    def inputs(tokens):
+        return dict(q=_bf(tokens, hk, dk), k=_bf(tokens, hk, dk), v=_bf(tokens, hv, dv),
+                    decay=torch.zeros((hv,) if head else (tokens, hv)), S=torch.zeros(5, hv, dv, dk),
+                    out=torch.zeros(tokens, hv, dv), err=torch.zeros(1, dtype=torch.int32),
+                    slots=torch.zeros(n, dtype=torch.int32))
+
+    def bad(tokens, good):
+        return [("q", good["q"].float()), ("k", good["k"].half()), ("v", good["v"].float()),
+                ("q", _bf(tokens - 1, hk, dk)), ("k", _bf(tokens, hk - 1, dk)), ("v", _bf(tokens - 1, hv, dv)),
+                ("decay", good["decay"].double()), ("decay", good["decay"].flatten()[:-1]),
+                ("S", good["S"].bfloat16()), ("S", good["S"][:4]), ("out", good["out"].bfloat16()),
+                ("out", good["out"][:-1]), ("err", good["err"].long()), ("err", good["err"][:0]),
+                ("slots", good["slots"].long()), ("slots", good["slots"][:-1])]
+
+    def step(c=cfg, **kw):
+        B.lq_linear_decode_step(c, num_slots=5, **kw)
+
+    def prefill(c=cfg, **kw):
+        B.lq_linear_prefill(c, tokens=T, num_slots=5, **kw)
+
+    _refused(step, inputs(n), bad(n, inputs(n)))
+    good = inputs(T)
+    good.update(offsets=torch.zeros(n + 1, dtype=torch.int32), fresh=torch.zeros(n, dtype=torch.int32),
+                workspace=torch.zeros(16, dtype=torch.uint8))
+    _refused(prefill, good, bad(T, good) + [
+        ("offsets", good["offsets"].long()), ("offsets", good["offsets"][:-1]), ("fresh", good["fresh"].bool()),
+        ("fresh", good["fresh"][:-1])])
+    # slices of a fused projection's rows: enough of them, and nothing past the last one's end
+    good.update(cut(rows))
+    prefill(c=fused, **good)
+    for name, x in cut(rows[:-1]).items():
+        with pytest.raises(ValueError, match=rf"^{name}: "):
+            prefill(c=fused, **{**good, name: x})
+    # other views of as many rows
+    packed = inputs(T)
+    packed.update(offsets=good["offsets"], q=_bf(T, hk * dk), k=_bf(T * hk * dk), v=_bf(1, T, hv, dv))
+    prefill(**packed)
+    prefill(**{**packed, "v": _bf(1, T + 1, hv, dv)})
+    with pytest.raises(ValueError, match="^v: "):
+        prefill(**{**packed, "v": _bf(1, T - 1, hv, dv)})
+
+
+def test_rotary_tensors_of_another_type_or_too_small_are_refused(on_host):
+    B, T = on_host, 5
+    cfg = B.make_rotary_config(4, 2, 64, 32)
+    good = dict(q=_bf(T, 4, 64), k=_bf(T, 2, 64), positions=torch.zeros(T, dtype=torch.int32),
+                table=torch.zeros(16, dtype=torch.int64), q_out=_bf(T, 4, 64), k_out=_bf(T, 2, 64))
+    _refused(lambda **kw: B.lq_rotary(cfg, T, **kw), good, [
+        ("q", good["q"].float()), ("k", good["k"][:-1]), ("positions", good["positions"].long()),
+        ("positions", good["positions"][:-1]), ("table", good["table"].int()), ("table", good["table"][:-1]),
+        ("q_out", good["q_out"].half()), ("k_out", good["k_out"][:, :1])])
+    B.lq_rotary(cfg, T, **{**good, "table": good["table"].view(torch.uint64)})
+    # what a configuration without k heads does not look at
+    B.lq_rotary(B.make_rotary_config(4, 0, 64, 32), T, **{**good, "k": torch.zeros(1), "k_out": None})
+
+
+def test_norm_tensors_of_another_type_or_too_small_are_refused(on_host):
+    B, T = on_host, 5
+    good = dict(x=_bf(T, 3, 20), out=torch.zeros(T, 3, 20), gate=_bf(T, 3, 20), weight=torch.zeros(3, 20),
+                bias=torch.zeros(3, 20))
+    cfg = B.make_norm_config(3, 20, in_bf16=True)
+    _refused(lambda **kw: B.lq_group_norm(cfg, T, **kw), good, [
+        ("x", good["x"].float()), ("x", good["x"][:-1]), ("out", good["out"].bfloat16()), ("out", good["out"][:-1]),
+        ("gate", good["gate"].float()), ("gate", good["gate"][:-1]), ("weight", good["weight"].bfloat16()),
+        ("weight", good["weight"][0]), ("bias", good["bias"].double()), ("bias", good["bias"][0])])
+    shared = B.make_norm_config(3, 20, in_bf16=True, shared_weight=True)
+    B.lq_group_norm(shared, T, **{**good, "weight": good["weight"][0].clone()})
+    with pytest.raises(ValueError, match="^err: "):
+        B.lq_get_error_word(torch.zeros(1))
