@@ -129,7 +129,7 @@ cudaError_t rotary_t(const RotaryParams &p, cudaStream_t st) {
   // instead split their heads over more blocks.
   int tok = 1;
   while (tok < kMaxTok && 2 * tok * half <= 2 * kNT && p.tokens / (2 * tok) >= 1184) tok *= 2;
-  const int gx = (p.tokens + tok - 1) / tok;
+  const int gx = (p.tokens - 1) / tok + 1;
   int gy = 1;
   while (gy * static_cast<int>(block.y) < heads && gx * gy < 296) gy *= 2;
   rotary_kernel<BF16, INTER, VEC><<<dim3(gx, gy), block, tok * half * sizeof(float2), st>>>(

@@ -792,3 +792,21 @@ def test_prefill_in_the_largest_calls_workspace(B, io):
         c.prefill(B, S, o, ws=ws[:size])
         c.check(o, S)
         assert bool((ws[size:] == 171).all())
+
+
+def test_rotary_of_the_most_tokens(B):
+    """2^31 - 1 tokens of one head of two channels, in place."""
+    n = (1 << 31) - 1
+    q = torch.ones((n, 1, 2), dtype=BF, device="cuda")
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    moved = torch.tensor([0, 1, 7, 8, n // 2, n - 9, n - 8, n - 1], device="cuda")
+    pos[moved] = torch.arange(1, 9, dtype=torch.int32, device="cuda")
+    table, _ = B.lq_rotary_table(2)
+    B.lq_rotary(B.make_rotary_config(1, 0, 2, 2), n, q, None, pos, table.cuda(), q, None)
+    a = torch.arange(1, 9, dtype=torch.float64, device="cuda")
+    want = torch.stack([torch.cos(a) - torch.sin(a), torch.cos(a) + torch.sin(a)], -1)
+    d = (q[moved, 0].double() - want).abs()
+    assert bool((d <= R * want.abs() + 32 * U).all())
+    q[moved] = 1.0  # position 0 turns nothing
+    for part in q.view(-1).split(1 << 28):
+        assert bool((part == 1.0).all())
