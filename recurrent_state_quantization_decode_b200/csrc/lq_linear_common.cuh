@@ -97,7 +97,7 @@ struct Segments {
   float *decays;   // workspace: [entry][Hv] the segments' whole decays
 
   __device__ __forceinline__ int pieces(int length) const {
-    return length <= whole ? 1 : (length + tokens - 1) / tokens;
+    return length <= whole ? 1 : (length - 1) / tokens + 1;
   }
 };
 
