@@ -810,3 +810,39 @@ def test_rotary_of_the_most_tokens(B):
     q[moved] = 1.0  # position 0 turns nothing
     for part in q.view(-1).split(1 << 28):
         assert bool((part == 1.0).all())
+
+
+# ---------------------------------------------------------------------------
+# Linear attention: alignments
+# ---------------------------------------------------------------------------
+
+def _inside(t, lead, fill):
+    """(a copy of t that starts `lead` values into its allocation, the guards on both sides)."""
+    n = t.numel()
+    whole = torch.full((lead + n + 64,), fill, dtype=t.dtype, device="cuda")
+    whole[lead:lead + n] = t.flatten()
+    return whole[lead:lead + n].view(t.shape), (whole[:lead], whole[lead + n:])
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (32, 128)])
+@pytest.mark.parametrize("io,out,lead", [(BF, BF, 1), (BF, BF, 8), (BF, F32, 1), (BF, F32, 4), (F32, F32, 1),
+                                         (F32, BF, 3)])
+def test_linear_alignments(B, dk, dv, io, out, lead):
+    """Outputs at any whole value, states and the workspace at any 16 bytes: the same bits as from the start
+    of an allocation, and nothing around them is written."""
+    for lengths in ([1500], [300, 0, 128, 41, 700], [1] * 7):
+        c = Linear(lengths, 1, 2, dk, dv, io, out, seed=dk + lead)
+        S0, o0 = c.S.clone(), c.new_out()
+        S1, around_S = _inside(c.S, 4, 5.0)
+        o1, around_o = _inside(c.new_out(), lead, 7.0)
+        if max(lengths) == 1:
+            for S, o in ((S0, o0), (S1, o1)):
+                B.lq_linear_decode_step(c.cfg(B), c.q, c.k, c.v, c.decay, S, c.num_slots, o, c.err, slots=c.slots)
+        else:
+            c.prefill(B, S0, o0)
+            ws, around_ws = _inside(c.workspace(B, c.cfg(B)), 16, 171)
+            c.prefill(B, S1, o1, ws=ws)
+            assert all(bool((x == 171).all()) for x in around_ws)
+        assert torch.equal(S0, S1) and torch.equal(o0, o1)
+        assert all(bool((x == 5.0).all()) for x in around_S) and all(bool((x == 7.0).all()) for x in around_o)
+        c.check(o1, S1)
