@@ -846,3 +846,97 @@ def test_linear_alignments(B, dk, dv, io, out, lead):
         assert torch.equal(S0, S1) and torch.equal(o0, o1)
         assert all(bool((x == 5.0).all()) for x in around_S) and all(bool((x == 7.0).all()) for x in around_o)
         c.check(o1, S1)
+
+
+# ---------------------------------------------------------------------------
+# Linear attention: the roundings of bf16 outputs
+# ---------------------------------------------------------------------------
+
+def _check_roundings(c, out):
+    """bf16 outputs of bf16 prompts round three things: the output itself (r of it), the state before the
+    chunk once (r of its values, in the product with q), and the decayed scores to two parts (2^-16);
+    everything else is within the fp32 bound u (2 * 128 + dk + 4) a chunk.  Value by value, and in the
+    2-norm with the two roundings to r as random ones of r / sqrt(3) each."""
+    q, k, v, d = c.q.double(), c.k.double(), c.v.double(), c.decay.double()
+    rep = c.hv // c.hk
+    want, size, state, square = (torch.zeros((c.n, c.hv, c.dv), dtype=torch.float64, device="cuda") for _ in range(4))
+    for b in range(c.b):
+        S = c.S[int(c.slots[b])].double()
+        if c.fresh is not None and int(c.fresh[b]):
+            S = torch.zeros_like(S)
+        A, first, G = S.abs(), S, torch.ones((c.hv,), dtype=torch.float64, device="cuda")
+        for t in range(c.off[b], c.off[b + 1]):
+            if (t - c.off[b]) % 128 == 0:
+                first, G = S, torch.ones_like(G)
+            a = d if c.decay_kind == "head" else d[t]
+            G = G * a
+            kk, qq = k[t].repeat_interleave(rep, 0), q[t].repeat_interleave(rep, 0)
+            S = a[:, None, None] * S + v[t][:, :, None] * kk[:, None, :]
+            A = a[:, None, None] * A + v[t].abs()[:, :, None] * kk.abs()[:, None, :]
+            want[t] = torch.einsum("hvk,hk->hv", S, qq)
+            size[t] = torch.einsum("hvk,hk->hv", A, qq.abs())
+            part = G[:, None, None] * first * qq[:, None, :]
+            state[t], square[t] = part.abs().sum(-1), (part * part).sum(-1)
+    chunks = -(-max(c.lengths) // 128)
+    fine = (2.0 ** -16 + U * (256 + c.dk + 4) * chunks) * size
+    do = (out[:c.n].double() - want).abs()
+    lim = R * want.abs() * (1 + R) + R * state + fine + 1e-30
+    assert bool((do <= lim).all()), float((do / lim).max())
+    norm = R / math.sqrt(3) * math.sqrt(float((want * want).sum() + square.sum())) + float(fine.norm())
+    assert float(do.norm()) <= norm, (float(do.norm()), norm)
+
+
+ROUNDINGS = {
+    "first_chunk": dict(lengths=[128, 77, 1, 100], hk=2, hv=4, dk=128, dv=128),
+    "first_chunk_d64": dict(lengths=[128, 50, 40], hk=1, hv=2, dk=64, dv=64, decay="head"),
+    "carried": dict(lengths=[700, 129, 256], hk=1, hv=2, dk=128, dv=128),
+    "slow": dict(lengths=[1500], hk=1, hv=2, dk=128, dv=64, decay="head"),
+}
+
+
+@pytest.mark.parametrize("name", sorted(ROUNDINGS))
+def test_prefill_roundings_of_bf16_outputs(B, name):
+    c = Linear(**ROUNDINGS[name], seed=21)
+    if name.startswith("first"):
+        c.fresh = torch.ones(c.b, dtype=torch.int32, device="cuda")
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o)
+    assert int(c.err) == 0
+    _check_roundings(c, o)
+
+
+def test_prefill_rows_of_one_score(B):
+    """Each output is one score's: nothing averages its roundings."""
+    c = Linear([128, 128, 90], 1, 2, 128, 128, seed=22)
+    c.fresh = torch.ones(c.b, dtype=torch.int32, device="cuda")
+    eye = torch.eye(128, device="cuda")
+    for b in range(c.b):
+        t = torch.arange(c.lengths[b], device="cuda")
+        c.k[c.off[b]:c.off[b + 1], 0] = eye[t].to(BF)
+        c.q[c.off[b]:c.off[b + 1], 0] = eye[(t - 5 * b).clamp(min=0)].to(BF)
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o)
+    assert int(c.err) == 0
+    _check_roundings(c, o)
+
+
+def test_prefill_of_a_state_nearly_orthogonal_to_q(B):
+    """A large state of which q sees a small difference: the outputs' error is the state's rounding, and
+    fp32 outputs do without it."""
+    for out in (BF, F32):
+        c = Linear([128, 300], 1, 2, 128, 128, out=out, seed=23)
+        c.S = c.S * 50.0
+        for b in range(c.b):
+            S = c.S[int(c.slots[b])]
+            S[:, :, 1::2] = -S[:, :, 0::2]  # q with equal pairs sees nothing of it
+            q = c.q[c.off[b]:c.off[b + 1]]
+            q[..., 1::2] = q[..., 0::2]
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o)
+        if out == BF:
+            assert int(c.err) == 0
+            _check_roundings(c, o)
+        else:
+            eo, _ = c.exact()
+            ao, _ = c.exact(absolute=True)
+            assert bool(((o[:c.n].double() - eo).abs() <= U * (2 * 384 + 132) * ao + U * eo.abs()).all())
