@@ -940,3 +940,80 @@ def test_prefill_of_a_state_nearly_orthogonal_to_q(B):
             eo, _ = c.exact()
             ao, _ = c.exact(absolute=True)
             assert bool(((o[:c.n].double() - eo).abs() <= U * (2 * 384 + 132) * ao + U * eo.abs()).all())
+
+
+# ---------------------------------------------------------------------------
+# Larger and odder calls
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_prefill_of_short_bf16_sequences(B, dk, dv, out):
+    """At most 32 tokens a sequence on average, a long one among them too: token by token, in segments."""
+    for lengths in ([20, 1, 31, 0, 7], [333] + [0, 1] * 20):
+        c = Linear(lengths, 2, 4, dk, dv, BF, out, fused=dv == 64, seed=dk * dv)
+        c.fresh = (torch.arange(c.b) % 3 == 1).to(torch.int32).cuda()
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o)
+        c.check(o, S)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_prefill_faults_among_many_sequences(B, io):
+    """More sequences than a warp looks at by itself: slots that cannot be used, and offsets past the rows."""
+    lengths = [40 + i % 90 for i in range(150)]
+    c = Linear(lengths, 1, 1, 32, 64, io, F32, seed=9)
+    own = c.slots.clone()
+    for change, report in (({149: -1, 3: -5}, False), ({140: int(own[0])}, True), ({0: c.num_slots, 131: 1 << 30}, True)):
+        c.slots = own.clone()
+        for i, s in change.items():
+            c.slots[i] = s
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o)
+        assert B.lq_get_error_word(c.err) == (B.LQ_ERR_DEVICE_BOUNDS if report else B.LQ_OK)
+        c.check(o, S, skip=tuple(change))
+    c.slots = own
+    c.offsets[150] = c.n + 1
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o)
+    assert B.lq_get_error_word(c.err) == B.LQ_ERR_DEVICE_BOUNDS
+    c.check(o, S, skip=(149,))
+
+
+@pytest.mark.parametrize("hk,hv,d,lengths", [(1, 640, 32, [300, 5]), (160, 160, 64, [150]), (7, 49, 32, [400, 129])])
+def test_prefill_head_counts(B, hk, hv, d, lengths):
+    """More heads than SMs, or none of their divisors."""
+    for io in (BF, F32):
+        c = Linear(lengths, hk, hv, d, d, io, F32, seed=hv)
+        S, o = c.S.clone(), c.new_out()
+        c.prefill(B, S, o)
+        c.check(o, S)
+
+
+@pytest.mark.parametrize("io,size", [(BF, 1 << 22), (F32, 1 << 21)])
+def test_prefill_rows_past_32_bit_offsets(B, io, size):
+    """Token rows so far apart that the last ones start more than 2^32 bytes and 2^30 values into them."""
+    c = Linear([257, 0, 300], 1, 2, 64, 64, io, F32, seed=2)
+    rows = torch.empty((c.n, size), dtype=io, device="cuda")
+    rows[:, :64], rows[:, 64:128], rows[:, 128:256] = c.q[:, 0], c.k[:, 0], c.v.flatten(1)
+    c.q, c.k, c.v = (rows[:, a:b].unflatten(1, (-1, 64)) for a, b in ((0, 64), (64, 128), (128, 256)))
+    S, o = c.S.clone(), c.new_out()
+    c.prefill(B, S, o)
+    c.check(o, S)
+
+
+def test_norm_past_32_bit_offsets(B):
+    """More than 2^31 values, in place."""
+    n, groups, size = 66001, 32, 1024
+    x = torch.ones((n, groups, size), dtype=BF, device="cuda")
+    at = torch.tensor([0, 1, n // 2, 65535, 65536, n - 2, n - 1], device="cuda")
+    some = torch.randn((len(at), groups, size), device="cuda").to(BF)
+    x[at] = some
+    B.lq_group_norm(B.make_norm_config(groups, size, act=B.LQ_ACT_NONE, in_bf16=True, out_bf16=True, eps=0.0), n, x, x)
+    want = some.double() / torch.sqrt((some.double() ** 2).mean(-1, keepdim=True))
+    d = (x[at].double() - want).abs()
+    assert bool((d <= want.abs() * (R + (size + 12) * U)).all())
+    x[at] = 1.0  # rows of ones stay ones
+    for part in x.view(-1).split(1 << 28):
+        assert bool((part == 1.0).all())
