@@ -13,8 +13,8 @@
  * Conventions (those of leapquant.h unless said otherwise):
  *  - Tensor arguments are device pointers of the current device; the library
  *    allocates nothing and keeps no global state; `stream` is a cudaStream_t
- *    (NULL = legacy default) and work is asynchronous on it.  Every call can
- *    be captured into a graph.
+ *    (NULL = legacy default) and work is asynchronous on it.  Every call but
+ *    lq_get_error_word, which waits, can be captured into a graph.
  *  - Argument errors are detected on the host before anything is launched:
  *    LQ_ERR_INVALID_ARG (null pointer, bad shape, stride or option),
  *    LQ_ERR_UNSUPPORTED (a size outside the stated range), LQ_ERR_MISALIGNED.
@@ -96,14 +96,23 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  *  one buffer for its largest call (78 MB at most up to 2^29 tokens, d = 128).
  *  Its contents matter during the call only; calls that may run at the same time,
  *  captured ones too, need one each.
- *  - bf16 prompts are taken in chunks of 128 tokens whose products run on the
- *    tensor cores with fp32 accumulation; states and fp32 outputs are fp32
- *    results (operands go in as exact sums of bf16 parts), bf16 outputs may
- *    see the state rounded once to bf16.  Decays enter as products over ranges
- *    of tokens, never as quotients: a decay of 0 (a reset) and long chains of
- *    small ones give exact zeros.  An infinite or NaN v shows in its
- *    channel of its sequence's outputs from the start of its chunk on, where the
- *    recurrence has it from its token on; nothing else sees it.
+ *  - bf16 prompts of more than 32 tokens a sequence on average (tokens > 32
+ *    batch) are taken in chunks of 128 tokens whose products run on the tensor
+ *    cores with fp32 accumulation; all others go token by token, which is slower
+ *    for a long sequence: among 255 empty ones 7,900 tokens, 32 heads, take 1,160
+ *    us and by themselves 136.  Such a sequence is better off in a call of its own.
+ *  - In chunks, states and fp32 outputs are fp32 results (operands go in as exact
+ *    sums of bf16 parts).  bf16 outputs see the state rounded once to bf16 and the
+ *    decayed scores to 2^-16: against 64 bits they are off by 1.72e-3 (2-norm, 24
+ *    prompts with carried states) to 2.0e-3 (32,768 tokens of slow decays), where
+ *    rounding exact outputs to bf16 alone gives 1.66e-3; where q sees only a small
+ *    difference of a large state the state's rounding is what is left, and fp32
+ *    outputs do without it.
+ *  - In chunks, decays enter as products over ranges of tokens, never as
+ *    quotients: a decay of 0 (a reset) and long chains of small ones give exact
+ *    zeros.  An infinite or NaN v shows, as NaN, in its channel of its sequence's
+ *    outputs from the start of its chunk on, where the recurrence has it from its
+ *    token on; nothing else sees it.  Token by token it shows from its token on.
  *  - out may not overlap the inputs. */
 size_t lq_linear_workspace_bytes(const lq_linear_config *cfg, int32_t tokens);
 lq_status lq_linear_prefill(const lq_linear_config *cfg, const void *q, const void *k,
@@ -132,7 +141,11 @@ typedef enum {
   LQ_ROPE_NTK = 2,    /* theta <- theta factor^(rot / (rot - 2)) */
   LQ_ROPE_PARTS = 3   /* by turns within the trained context: w_i f_i + (1 - w_i) f_i / factor,
                          w_i = clamp((trained f_i / 2 pi - slow) / (fast - slow), 0, 1);
-                         magnitude m = 0.1 ln(factor) + 1 for factor > 1 */
+                         magnitude m = 0.1 ln(factor) + 1 for factor > 1.  The ramp is linear in
+                         turns.  Checkpoints whose code ramps over the pair's index i between two
+                         bounds instead (often rounded to whole pairs) have other frequencies in
+                         between: fill the table from those, entry by entry as lq_rotary_table
+                         says */
 } lq_rope_scaling;
 
 typedef struct {
@@ -177,7 +190,9 @@ lq_status lq_rotary(const lq_rotary_config *cfg, int32_t tokens, const void *q, 
  *   y = n(x) act(z)          with a gate z
  *   y = n(x act(z))          with a gate z and gate_before
  * Statistics are fp32 over the group's values held on chip, the variance from
- * the centred values.
+ * the centred values (a group whose squares add up past fp32's range comes out
+ * as zeros).  Rows move in pieces of 16 bytes where size, strides and addresses
+ * are whole pieces, else value by value, at 2 to 20 times the time.
  * ---------------------------------------------------------------------- */
 
 typedef enum { LQ_NORM_RMS = 0, LQ_NORM_MEAN = 1 } lq_norm_kind;
@@ -197,8 +212,9 @@ typedef struct {
 } lq_norm_config;
 
 /* x [tokens][groups][size]; gate: nullable, as x; weight: nullable fp32;
- * bias: nullable fp32 [groups][size]; out may be x or the gate itself (with
- * the same type and stride). */
+ * bias: nullable fp32 [groups][size], also with a shared weight (a shared bias
+ * is repeated there by the caller); out may be x or the gate itself (with the
+ * same type and stride). */
 lq_status lq_group_norm(const lq_norm_config *cfg, int32_t tokens, const void *x,
                         const void *gate, const float *weight, const float *bias, void *out,
                         void *stream);

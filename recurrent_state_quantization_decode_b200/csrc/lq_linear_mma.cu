@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kNT, 1)
     set_registers_down<64>();
     // The issuing warps run as a whole, which leaves their operands' addresses in
     // uniform registers, and one lane issues (by a single thread's code 32,768
-    // tokens, 32 heads took 476 us where this takes 451).
+    // tokens, 32 heads took 476 us where this takes 451, in short bursts of calls;
+    // long runs are at the power cap: 492 to 520).
     const uint32_t lead = tc::elect();
     if (warp == 20) {
       constexpr uint32_t kShapeQK = tc::product_shape(kC, kC, false, false);
@@ -743,7 +744,10 @@ __global__ void __launch_bounds__(kNT, 1)
       arrive_warp(at(kGrownRead));
       return true;
     };
-    // the state's bf16 copy: row e of [DVP][DKP]
+    // The state's bf16 copy: row e of [DVP][DKP].  Of three parts, S being the
+    // same for all, the compiler keeps the earlier ones and remainders across the
+    // waits in between: with DKP = 128 the fp32-output forms spill for it (786
+    // bytes stored and 1,196 loaded a thread; the bf16 form 68 and 244).
     auto copy_state = [&](auto part) {
       constexpr int kPart = decltype(part)::value;
       const uint32_t row = anew(base) + T::kState + f0 / 64 * (DVP * 128) + e * 128;

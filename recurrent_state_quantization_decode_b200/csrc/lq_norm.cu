@@ -181,8 +181,11 @@ cudaError_t norm_u(const NormParams &p, int lanes, int64_t grid, cudaStream_t st
 // that all run at once and keep every lane on one group: a grid that is a
 // multiple of groups / gcd(groups, rows of a block).  Then two rows at a time,
 // but for fp32 with a gate, where a row's own loads are enough: 16,384 x 32 x
-// 128, fp32 to bf16, 76 us with two and 90 with one; with a gate and fp32 130
-// and 105; bf16 throughout 63 and 72, with a gate 78 and 82.
+// 128, fp32 to bf16, 76 us with two and 90 with one (70 and 80 us with two by
+// short bursts of calls and by long runs at the power cap); with a gate and fp32
+// 130 and 105; bf16 throughout 63 and 72, with a gate 78 and 82.  Value by value
+// (VEC = 1) neither side leads: 5,216 x 32 x 201, bf16, 92 with two and 105 with
+// one, with a gate 155 and 139; 61,680 x 32 x 17, 124 and 120, 152 and 163.
 template <bool BF16, bool OUT16, bool GATE, int VEC, int CPL, bool BLOCK>
 cudaError_t norm_t(const NormParams &p, int lanes, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.groups;
