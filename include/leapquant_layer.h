@@ -102,12 +102,9 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  *    for a long sequence: among 255 empty ones 7,900 tokens, 32 heads, take 1,160
  *    us and by themselves 136.  Such a sequence is better off in a call of its own.
  *  - In chunks, states and fp32 outputs are fp32 results (operands go in as exact
- *    sums of bf16 parts).  bf16 outputs see the state rounded once to bf16 and the
- *    decayed scores to 2^-16: against 64 bits they are off by 1.72e-3 (2-norm, 24
- *    prompts with carried states) to 2.0e-3 (32,768 tokens of slow decays), where
- *    rounding exact outputs to bf16 alone gives 1.66e-3; where q sees only a small
- *    difference of a large state the state's rounding is what is left, and fp32
- *    outputs do without it.
+ *    sums of bf16 parts).  bf16 outputs see the state and the decayed scores to
+ *    2^-16, well below their own rounding: 1.66e-3 against 64 bits (2-norm), as
+ *    exact outputs have it.
  *  - In chunks, decays enter as products over ranges of tokens, never as
  *    quotients: a decay of 0 (a reset) and long chains of small ones give exact
  *    zeros.  An infinite or NaN v shows, as NaN, in its channel of its sequence's

@@ -34,10 +34,13 @@
 // state is an fp32 result; S' = G S + increment is rounded once or twice in
 // fp32 (G as a sum of two floats: an error in G would be the same in every
 // chunk and add up).  W o P and S meet bf16 operands in the products for O.
-// With fp32 outputs they go in as three exact parts.  With bf16 outputs W o P
-// goes in as two (to 2^-16: few scores can make up a whole row of O, so that
-// their rounding would show), and S, whose roundings average over the key
-// channels, as one, to 2^-8 like the outputs themselves.
+// With fp32 outputs they go in as three exact parts, with bf16 outputs as two, to
+// 2^-16, which leaves the rounding of O itself: 1.66e-3 against 64 bits on 24
+// prompts and on 32,768 tokens, where S as one part (2^-8) gave 1.72e-3 and
+// 2.0e-3, and more where q sees only a small difference of a large state.  The
+// second part of S costs 9 % (24 prompts of 20,011 tokens, 32 heads, 260 -> 285
+// us; 32,768 tokens 507 -> 554); a third one of W o P, which leaves the error as
+// it is, would take 298 and 594.
 
 #include <atomic>
 #include <cstddef>
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kNT, 1)
                          const __grid_constant__ CUtensorMap mo) {
   using T = Tiles<DKP, DVP>;
   constexpr int PARTS = F32OUT ? 3 : 2;   // bf16 parts of W o P
-  constexpr int SPARTS = F32OUT ? 3 : 1;  // and of the state in Q S^T
+  constexpr int SPARTS = F32OUT ? 3 : 2;  // and of the state in Q S^T
   constexpr int RING = F32OUT ? 1 : 2;    // slots of the ring
   constexpr int SWARPS = DVP / 16, VWARPS = DVP / 32;  // warps with the state, with w V
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -744,12 +747,17 @@ __global__ void __launch_bounds__(kNT, 1)
       arrive_warp(at(kGrownRead));
       return true;
     };
-    // The state's bf16 copy: row e of [DVP][DKP].  Of three parts, S being the
-    // same for all, the compiler keeps the earlier ones and remainders across the
-    // waits in between: with DKP = 128 the fp32-output forms spill for it (786
-    // bytes stored and 1,196 loaded a thread; the bf16 form 68 and 244).
+    // The state's bf16 copy, a part at a time: row e of [DVP][DKP].  S being the
+    // same for all parts, the compiler would keep earlier ones and remainders across
+    // the waits in between, and spill for it with DKP = 128 (fp32 outputs: 786 bytes
+    // stored and 1,196 loaded a thread, bf16 350 and 700): there S is hidden from it,
+    // which leaves 60 to 80 and 220 to 256.
     auto copy_state = [&](auto part) {
       constexpr int kPart = decltype(part)::value;
+      if constexpr (kPart > 0 && DKP == 128) {
+#pragma unroll
+        for (int f = 0; f < kF; ++f) asm volatile("" : "+f"(S[f]));
+      }
       const uint32_t row = anew(base) + T::kState + f0 / 64 * (DVP * 128) + e * 128;
 #pragma unroll
       for (int f = 0; f < kF; f += 8) {
@@ -854,17 +862,17 @@ __global__ void __launch_bounds__(kNT, 1)
         if (c > 0 && !(ok = wait_warp(at(kQSDone), (c - 1) & 1, dead, p.err))) break;
         if (holds) {
           copy_state(std::integral_constant<int, 0>());
+          // its further parts once the products with the last one are done; those
+          // need the last chunk's outputs out of the way
+          if (c > 0 && !(ok = outputs(c - 1))) break;
+          if (!(ok = wait_warp(at(kQSPart), F32OUT ? 0 : c & 1, dead, p.err))) break;
+          copy_state(std::integral_constant<int, 1>());
           if constexpr (F32OUT) {
-            // its further parts once the products with the last one are done;
-            // those need the last chunk's outputs out of the way
-            if (c > 0 && !(ok = outputs(c - 1))) break;
-            if (!(ok = wait_warp(at(kQSPart), 0, dead, p.err))) break;
-            copy_state(std::integral_constant<int, 1>());
             if (!(ok = wait_warp(at(kQSPart), 1, dead, p.err))) break;
             copy_state(std::integral_constant<int, 2>());
           }
         }
-        if ((!F32OUT || !holds) && c > 0 && !(ok = outputs(c - 1))) break;
+        if (!holds && c > 0 && !(ok = outputs(c - 1))) break;
         // G (Q S^T)
         if (!(ok = wait_warp(at(kQSDone), c & 1, dead, p.err))) break;
         tc::after_sync();
