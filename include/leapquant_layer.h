@@ -99,8 +99,8 @@ lq_status lq_linear_decode_step(const lq_linear_config *cfg, const void *q, cons
  *  - bf16 prompts of more than 32 tokens a sequence on average (tokens > 32
  *    batch) are taken in chunks of 128 tokens whose products run on the tensor
  *    cores with fp32 accumulation; all others go token by token, which is slower
- *    for a long sequence: among 255 empty ones 7,900 tokens, 32 heads, take 1,160
- *    us and by themselves 136.  Such a sequence is better off in a call of its own.
+ *    for a long sequence: among 255 empty ones 7,900 tokens, 32 heads, take 1,154
+ *    us and by themselves 155.  Such a sequence is better off in a call of its own.
  *  - In chunks, states and fp32 outputs are fp32 results (operands go in as exact
  *    sums of bf16 parts).  bf16 outputs see the state and the decayed scores to
  *    2^-16, well below their own rounding: 1.66e-3 against 64 bits (2-norm), as

@@ -82,11 +82,12 @@ lq_status check_linear_io(const lq_linear_config *c, lq::LinParams *p, bool inpu
 
 // Which prompt kernel a call takes: bf16 inputs go to the tensor cores, unless
 // sequences are so short on average that a chunk of 128 tokens would be mostly
-// padding (64 sequences x 32 heads, d = 128: 16 tokens each 122 us token by
-// token and 223 us in chunks, 36 each 223 and 228, 64 each 358 and 232).  The
-// lengths themselves are on the device: a long sequence among many empty ones
-// goes token by token by this rule, though chunks would be faster (7,900 tokens
-// and 255 empty sequences, 32 heads: 1,160 us; by itself, in chunks, 136).
+// padding (64 sequences x 32 heads, d = 128: 16 tokens each 119 us token by
+// token and 235 us in chunks, 32 each 198 and 240, 36 each 221 and 240, 48 each
+// 279 and 243, 64 each 357 and 249).  The lengths themselves are on the device: a
+// long sequence among many empty ones goes token by token by this rule, though
+// chunks would be faster (7,900 tokens and 255 empty sequences, 32 heads: 1,154
+// us; by itself, in chunks, 155).
 bool by_chunks(const lq::LinParams &p) {
   return p.in_bf16 != 0 && p.tokens > 32 * static_cast<int64_t>(p.B);
 }

@@ -105,8 +105,8 @@ struct Segments {
 // the long sequences first: one that starts late adds its whole time to the
 // call's.  Pass 0 takes those whole ones, 1 the cut ones and all of more than
 // half a segment, 2 the rest.  24 prompts of 20,011 tokens, 32 heads, the longest
-// 1.4 segments: in the call's order 244 us with it first and 392 us with it last,
-// in passes 239 to 258 us in seven orders.
+// 1.4 segments: in the call's order 268 us with it first and 417 us with it last,
+// in passes 259 to 276 us in seven orders.
 //
 // A sequence's blocks count in its pass's 10 bits of a sum.  There are fewer than
 // 1,024: with several sequences a segment is an SM's share of the call at least,

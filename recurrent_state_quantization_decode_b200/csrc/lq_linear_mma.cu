@@ -305,8 +305,9 @@ __global__ void __launch_bounds__(kNT, 1)
     set_registers_down<64>();
     // The issuing warps run as a whole, which leaves their operands' addresses in
     // uniform registers, and one lane issues (by a single thread's code 32,768
-    // tokens, 32 heads took 476 us where this takes 451, in short bursts of calls;
-    // long runs are at the power cap: 492 to 520).
+    // tokens, 32 heads took 476 us where this took 451, with the state in one part
+    // and in short bursts of calls; with two parts now 478, and 532 in long runs,
+    // which the power cap slows down).
     const uint32_t lead = tc::elect();
     if (warp == 20) {
       constexpr uint32_t kShapeQK = tc::product_shape(kC, kC, false, false);
@@ -1018,9 +1019,9 @@ int linear_segment(const LinParams &p) {
 // The longest sequence that stays whole.  The states' pass makes a cut sequence
 // cost half as much again, so among several, one of up to one and a half shares
 // of an SM takes no longer whole if its blocks start first (Rank): 24 prompts of
-// 20,011 tokens in all, 32 heads, the longest 1.4 shares, 262 us whole and 336 us
-// cut; 9 prompts of 7,000 tokens, fp32 outputs, the longest 1.95 shares, 284 us
-// whole and 223 us cut.
+// 20,011 tokens in all, 32 heads, the longest 1.4 shares, 271 us whole and 345 us
+// cut (fp32 outputs 405 and 449); 9 prompts of 7,000 tokens, the longest 1.95
+// shares, fp32 outputs, 217 us whole and 191 us cut (bf16 outputs 140 and 147).
 static int longest_whole(const LinParams &p, int segment) {
   return p.B > 1 && p.B <= kRankedMost && segment < p.tokens ? segment + segment / 2 : segment;
 }
